@@ -364,6 +364,100 @@ mf_status mf_mmdit_block_bwd(const mf_bf16* dy, const mf_bf16* x, const mf_bf16*
                              void* workspace, size_t ws_bytes, cudaStream_t stream);
 size_t mf_mmdit_bwd_workspace_size(int32_t T, int32_t S, int32_t H, int32_t D, int32_t F);
 
+/* ---- A pre-norm MLP branch with its own weights and biases: the layer norm, the
+ * linear layer with its epilogue, their backward passes, and activations kept for
+ * the backward in 8 bits [norm], [fuse], [train]. The pages name modality-specific
+ * weights and fused chains, not these forms; they are the usual ones. m is the
+ * token's modality, tok_mod[t] (0 image, 1 text) from mf_pack_build.
+ *
+ * Activation checkpoints in 8 bits: q [T][C] int8 codes and scale [T][ceil(C /
+ * MF_ACT8_BLOCK)] fp32, one scale per token and MF_ACT8_BLOCK consecutive
+ * channels (the last block of a row may be shorter). With amax a block's largest
+ * magnitude, scale = amax / 127 and q = round-half-even(x * (127 / amax)) in fp32
+ * (|q| <= 127): the value q * scale is within scale / 2 of x (up to fp32
+ * rounding). A block with amax < 2^-100 is stored as zeros; a block that holds an
+ * infinity or NaN gets a NaN scale and so reads back as NaN. C a multiple of 8,
+ * C <= 2^20. x must not overlap q or scale. */
+#define MF_ACT8_BLOCK 128
+mf_status mf_act8_quantize(const mf_bf16* x, int32_t T, int32_t C, int8_t* q, float* scale,
+                           cudaStream_t stream);
+
+/* y = act(q * scale) [T][C] in bf16, act one of MF_ACT_NONE, MF_ACT_GELU,
+ * MF_ACT_SILU: an MLP's hidden activation comes back from the kept pre-activation.
+ * y must not overlap q or scale. */
+mf_status mf_act8_dequantize(const int8_t* q, const float* scale, int32_t T, int32_t C,
+                             int32_t act, mf_bf16* y, cudaStream_t stream);
+
+/* Modality-specific layer norm with weights [norm]: y[t] = (x[t] - mean) * rstd *
+ * gamma[m] + beta[m], mean and (population) variance over the row's hid channels,
+ * rstd = 1 / sqrt(var + eps). x, y: [T][hid] bf16 (must not overlap); gamma, beta:
+ * [2][hid] fp32, image first; stats: NULL, or [T][2] fp32 (mean, rstd) for the
+ * backward. hid a multiple of 8, hid <= 8192 (else MF_ERR_UNSUPPORTED). fp32
+ * arithmetic, one rounding to bf16. A tok_mod above 1 is recorded as
+ * MF_ERR_INVALID and its row left unwritten. */
+mf_status mf_layer_norm(const mf_bf16* x, const float* gamma, const float* beta,
+                        const uint8_t* tok_mod, int32_t T, int32_t hid, float eps, mf_bf16* y,
+                        float* stats, cudaStream_t stream);
+
+/* Backward of mf_layer_norm [norm], [train]: with xhat = (x - mean) * rstd from
+ * stats and g = dy * gamma[m],
+ *   dx = resid + (g - mean(g) - xhat * mean(g * xhat)) * rstd,
+ *   dgamma[m] = sum dy * xhat, dbeta[m] = sum dy over the modality's tokens
+ * (zero for a modality without tokens). The forward's input is given as x
+ * ([T][hid] bf16) or as its 8-bit checkpoint (x8, x_scale), the other NULL. resid:
+ * NULL (0) or [T][hid] bf16, the gradient on the residual path; dx may equal resid
+ * (in place) and overlaps no other argument. dgamma, dbeta: [2][hid] fp32,
+ * overwritten; sums in a fixed order without atomics, so repeated calls give the
+ * same bits. ws_bytes >= mf_layer_norm_bwd_workspace_size(T, hid). Bad tok_mod as
+ * for mf_layer_norm (the row takes no part in the sums either). */
+mf_status mf_layer_norm_bwd(const mf_bf16* dy, const mf_bf16* x, const int8_t* x8,
+                            const float* x_scale, const float* gamma, const float* stats,
+                            const uint8_t* tok_mod, const mf_bf16* resid, int32_t T, int32_t hid,
+                            mf_bf16* dx, float* dgamma, float* dbeta, void* workspace,
+                            size_t ws_bytes, cudaStream_t stream);
+size_t mf_layer_norm_bwd_workspace_size(int32_t T, int32_t hid);
+
+/* Modality-specific linear layer with its epilogue in the product's kernel
+ * [norm], [fuse]: z[t] = x[t] W[m]^T + bias[m], out[t] = act(z[t]) + resid[t].
+ * x: [T][K] bf16; W: [2][N][K] bf16 (image first); bias: NULL or [2][N] fp32;
+ * resid: NULL or [T][N] bf16; act: MF_ACT_NONE, MF_ACT_GELU (tanh form) or
+ * MF_ACT_SILU. out: [T][N] bf16. z: NULL, or [T][N] bf16 to keep the
+ * pre-activation; z8, z_scale: both NULL, or its 8-bit checkpoint (taken from the
+ * fp32 z, which is not rounded to bf16 first). tcgen05 tensor cores, fp32
+ * accumulation and epilogue, one rounding per output. out may equal resid; no
+ * output overlaps anything else. K and N multiples of 8 up to 2^20, T <= 131072
+ * (else MF_ERR_UNSUPPORTED). tok_mod and desc as for mf_modality_linear; a row
+ * whose tok_mod is neither 0 nor 1 is left unwritten. */
+#define MF_ACT_SILU 2
+mf_status mf_linear_fused(const mf_bf16* x, const mf_bf16* W, const float* bias,
+                          const mf_bf16* resid, const uint8_t* tok_mod,
+                          const mf_sample_desc* desc, int32_t S, int32_t K, int32_t N, int32_t act,
+                          mf_bf16* z, int8_t* z8, float* z_scale, mf_bf16* out,
+                          cudaStream_t stream);
+
+/* Backward of mf_linear_fused [norm], [train] for the loss gradient dout of out
+ * ([T][N] bf16; the gradient of resid is dout itself):
+ *   dz = dout * act'(z), dx[t] = dz[t] W[m],
+ *   dW[m] = sum dz[t]^T x[t], db[m] = sum dz[t] over the modality's tokens
+ * (zero for a modality without tokens). dx [T][K] bf16, dW [2][N][K] bf16 and
+ * db [2][N] fp32: any may be NULL, not all. The input is given as x (bf16) or as
+ * its 8-bit checkpoint (x8, x_scale), the other NULL; dW alone reads it. The
+ * pre-activation is given as z or (z8, z_scale) in the same way; with MF_ACT_NONE
+ * it is not read. W is read for dx alone. dz is rounded to bf16 as the operand of
+ * both products (db sums it unrounded), an 8-bit x is rounded to bf16 as an
+ * operand; fp32 accumulation in a fixed order, no atomics. Rows of the other
+ * modality take no part in dW[m] whatever they hold. No output overlaps anything
+ * else. ws_bytes >= mf_linear_fused_bwd_workspace_size(T, K, N). Shapes, tok_mod
+ * and desc as for the forward (a tok_mod above 1 is recorded as MF_ERR_INVALID
+ * where db or act' is computed). */
+mf_status mf_linear_fused_bwd(const mf_bf16* dout, const mf_bf16* x, const int8_t* x8,
+                              const float* x_scale, const mf_bf16* W, const mf_bf16* z,
+                              const int8_t* z8, const float* z_scale, const uint8_t* tok_mod,
+                              const mf_sample_desc* desc, int32_t S, int32_t K, int32_t N,
+                              int32_t act, mf_bf16* dx, mf_bf16* dW, float* db, void* workspace,
+                              size_t ws_bytes, cudaStream_t stream);
+size_t mf_linear_fused_bwd_workspace_size(int32_t T, int32_t K, int32_t N);
+
 /* Mage-VAE conv block [vae], [vfuse]: the fully convolutional VAE's repeated
  * blocks and their fused normalization - activation - residual chains. The
  * pages give neither the wiring nor the widths; the library takes the diffusion

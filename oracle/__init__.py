@@ -71,6 +71,16 @@ from .mf_oracle import (  # noqa: F401
     varlen_attention,
     varlen_attention_bwd,
 )
+from .mlp_oracle import (  # noqa: F401
+    act8_quantize,
+    act8_values,
+    layer_norm_affine,
+    layer_norm_affine_bwd,
+    linear_fused,
+    linear_fused_bwd,
+    mlp_act,
+    mlp_act_grad,
+)
 from .vae_oracle import (  # noqa: F401
     conv3x3,
     group_norm,

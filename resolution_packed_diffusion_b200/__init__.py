@@ -101,6 +101,15 @@ _SIGS = {
     "mf_vae_res_block": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P,
                               _SZ, _P]),
     "mf_vae_block_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "mf_act8_quantize": (_I, [_P, _I, _I, _P, _P, _P]),
+    "mf_act8_dequantize": (_I, [_P, _P, _I, _I, _I, _P, _P]),
+    "mf_layer_norm": (_I, [_P, _P, _P, _P, _I, _I, _F, _P, _P, _P]),
+    "mf_layer_norm_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _SZ, _P]),
+    "mf_layer_norm_bwd_workspace_size": (_SZ, [_I, _I]),
+    "mf_linear_fused": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "mf_linear_fused_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P,
+                                 _P, _P, _SZ, _P]),
+    "mf_linear_fused_bwd_workspace_size": (_SZ, [_I, _I, _I]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -416,3 +425,74 @@ def mf_vae_res_block(x, gamma1, beta1, W1, c1, gamma2, beta2, W2, c2, N: int, H:
                                 _ptr(gamma2), _ptr(beta2), _ptr(W2), _ptr(c2), N, H, W, C, G,
                                 eps, _ptr(y), _ptr(workspace), ws_bytes, _stream(stream)),
            "mf_vae_res_block")
+
+
+MF_ACT_SILU = 2
+MF_ACT8_BLOCK = 128  # channels that share one scale of an 8-bit checkpoint
+
+
+def _descs(descs) -> Tuple[ctypes.Array, int]:
+    """(descriptor array, number of samples): an array from make_descs is taken as
+    it is, so that a caller with a fixed pack builds it once."""
+    if isinstance(descs, ctypes.Array):
+        return descs, len(descs)
+    rows = list(descs)
+    return make_descs(rows), len(rows)
+
+
+def mf_act8_quantize(x, T: int, C: int, q, scale, stream=None) -> None:
+    """8-bit checkpoint of x [T][C]: codes q int8 [T][C] and scale fp32
+    [T][ceil(C / MF_ACT8_BLOCK)]."""
+    _check(lib.mf_act8_quantize(_ptr(x), T, C, _ptr(q), _ptr(scale), _stream(stream)),
+           "mf_act8_quantize")
+
+
+def mf_act8_dequantize(q, scale, T: int, C: int, act: int, y, stream=None) -> None:
+    """y = act(q * scale) in bf16."""
+    _check(lib.mf_act8_dequantize(_ptr(q), _ptr(scale), T, C, act, _ptr(y), _stream(stream)),
+           "mf_act8_dequantize")
+
+
+def mf_layer_norm(x, gamma, beta, tok_mod, T: int, hid: int, eps: float, y, stats=None,
+                  stream=None) -> None:
+    """y = LN(x) * gamma[m] + beta[m]; stats [T][2] fp32 (mean, rstd) or None."""
+    _check(lib.mf_layer_norm(_ptr(x), _ptr(gamma), _ptr(beta), _ptr(tok_mod), T, hid, eps,
+                             _ptr(y), _ptr(stats), _stream(stream)), "mf_layer_norm")
+
+
+def mf_layer_norm_bwd_workspace_size(T: int, hid: int) -> int:
+    return int(lib.mf_layer_norm_bwd_workspace_size(T, hid))
+
+
+def mf_layer_norm_bwd(dy, x, x8, x_scale, gamma, stats, tok_mod, resid, T: int, hid: int, dx,
+                      dgamma, dbeta, workspace, ws_bytes: int, stream=None) -> None:
+    """The input is x (bf16) or (x8, x_scale), an 8-bit checkpoint; the other is None."""
+    _check(lib.mf_layer_norm_bwd(_ptr(dy), _ptr(x), _ptr(x8), _ptr(x_scale), _ptr(gamma),
+                                 _ptr(stats), _ptr(tok_mod), _ptr(resid), T, hid, _ptr(dx),
+                                 _ptr(dgamma), _ptr(dbeta), _ptr(workspace), ws_bytes,
+                                 _stream(stream)), "mf_layer_norm_bwd")
+
+
+def mf_linear_fused(x, W, bias, resid, tok_mod, descs, K: int, N: int, act: int, z, z8, z_scale,
+                    out, stream=None) -> None:
+    """out = act(x W[m]^T + bias[m]) + resid; z (bf16) and / or (z8, z_scale) keep
+    the pre-activation. ``descs`` as for mf_modality_linear, or a make_descs array."""
+    arr, S = _descs(descs)
+    _check(lib.mf_linear_fused(_ptr(x), _ptr(W), _ptr(bias), _ptr(resid), _ptr(tok_mod),
+                               ctypes.cast(arr, _P), S, K, N, act, _ptr(z), _ptr(z8),
+                               _ptr(z_scale), _ptr(out), _stream(stream)), "mf_linear_fused")
+
+
+def mf_linear_fused_bwd_workspace_size(T: int, K: int, N: int) -> int:
+    return int(lib.mf_linear_fused_bwd_workspace_size(T, K, N))
+
+
+def mf_linear_fused_bwd(dout, x, x8, x_scale, W, z, z8, z_scale, tok_mod, descs, K: int, N: int,
+                        act: int, dx, dW, db, workspace, ws_bytes: int, stream=None) -> None:
+    """Gradients of mf_linear_fused: dx, dW and db, any of them None. The input is x
+    or (x8, x_scale), the pre-activation z or (z8, z_scale)."""
+    arr, S = _descs(descs)
+    _check(lib.mf_linear_fused_bwd(_ptr(dout), _ptr(x), _ptr(x8), _ptr(x_scale), _ptr(W), _ptr(z),
+                                   _ptr(z8), _ptr(z_scale), _ptr(tok_mod), ctypes.cast(arr, _P), S,
+                                   K, N, act, _ptr(dx), _ptr(dW), _ptr(db), _ptr(workspace),
+                                   ws_bytes, _stream(stream)), "mf_linear_fused_bwd")

@@ -1,0 +1,134 @@
+// act8.cu -- activation checkpoints in 8 bits: a [T][C] bf16 activation kept for
+// the backward as int8 codes with one fp32 scale per token and 128 channels,
+//   s = amax / 127, q = rint(x * (127 / amax)), x ~ q s,
+// and read back through the activation that followed it, y = act(q s).
+//
+// Why this form: the error of a code is at most s / 2 = amax / 254, relative RMS
+// about 0.6% for a normal block (an 8-bit float with three mantissa bits has
+// 2.6%); 128 channels keep one outlier from costing a whole row its precision at
+// 3% extra bytes. The picx.dev "Mage-Flow" summary (Methodology > Training
+// Infrastructure) names training under a memory budget; the format is this
+// library's own.
+//
+// Both kernels are bound by HBM (3 bytes a value plus the scales). Sixteen lanes
+// hold a block, eight channels (16 bytes) each, so two blocks to a warp and a
+// maximum by four shuffles; every thread takes kUnroll blocks whose loads are all
+// issued before the first is used.
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "act8.cuh"
+#include "mlp_internal.h"
+
+namespace mf {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;
+constexpr int kLanes = kAct8Block / 8;           // lanes of a block
+constexpr int kPerCta = kThreads / kLanes;       // blocks a CTA takes per step
+
+// Largest |x| of eight bf16 values as a 15-bit pattern (NaN above infinity).
+__device__ __forceinline__ uint32_t absmax_bits(const uint4& u) {
+  const uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
+                              __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+  return max(m & 0xFFFFu, m >> 16);
+}
+
+// items = T * nb blocks in row order; item i is block i % nb of row i / nb.
+__global__ void __launch_bounds__(kThreads) act8_quantize_kernel(const mf_bf16* __restrict__ x,
+                                                                 int64_t items, int nb, int C,
+                                                                 int8_t* __restrict__ q,
+                                                                 float* __restrict__ scale) {
+  const int lane = threadIdx.x % kLanes;
+  const int64_t base = blockIdx.x * static_cast<int64_t>(kPerCta * kUnroll) + threadIdx.x / kLanes;
+  uint4 v[kUnroll];
+  int64_t off[kUnroll];
+  bool in[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t item = base + u * kPerCta;
+    const int64_t row = item / nb;
+    const int c = static_cast<int>(item - row * nb) * kAct8Block + lane * 8;
+    in[u] = item < items && c < C;
+    off[u] = row * C + c;
+    v[u] = in[u] ? __ldcs(reinterpret_cast<const uint4*>(x + off[u])) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    uint32_t m = absmax_bits(v[u]);
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float s, inv, f[8];
+    act8_scale(__uint_as_float(m << 16), s, inv);
+    bf16x8_unpack(v[u], f);
+    if (in[u])
+      __stcs(reinterpret_cast<uint2*>(q + off[u]), make_uint2(act8_code4(f, inv), act8_code4(f + 4, inv)));
+    const int64_t item = base + u * kPerCta;
+    if (lane == 0 && item < items) scale[item] = s;
+  }
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(kThreads) act8_dequantize_kernel(const int8_t* __restrict__ q,
+                                                                   const float* __restrict__ scale,
+                                                                   int64_t items, int nb, int C,
+                                                                   mf_bf16* __restrict__ y) {
+  const int lane = threadIdx.x % kLanes;
+  const int64_t base = blockIdx.x * static_cast<int64_t>(kPerCta * kUnroll) + threadIdx.x / kLanes;
+  uint2 v[kUnroll];
+  float s[kUnroll];
+  int64_t off[kUnroll];
+  bool in[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t item = base + u * kPerCta;
+    const int64_t row = item / nb;
+    const int c = static_cast<int>(item - row * nb) * kAct8Block + lane * 8;
+    in[u] = item < items && c < C;
+    off[u] = row * C + c;
+    v[u] = in[u] ? __ldcs(reinterpret_cast<const uint2*>(q + off[u])) : make_uint2(0, 0);
+    s[u] = item < items ? __ldg(scale + item) : 0.f;
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    float f[8];
+    act8_load(v[u], s[u], f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = act_fwd<ACT>(f[e]);
+    if (in[u]) __stcs(reinterpret_cast<uint4*>(y + off[u]), bf16x8_pack(f));
+  }
+}
+
+unsigned grid_of(int64_t items) {
+  return static_cast<unsigned>((items + kPerCta * kUnroll - 1) / (kPerCta * kUnroll));
+}
+
+}  // namespace
+
+// T <= 2^24 and nb <= 2^13 keep the grid within 2^31 (one CTA per 64 blocks).
+cudaError_t launch_act8_quantize(const mf_bf16* x, int32_t T, int32_t C, int8_t* q, float* scale,
+                                 cudaStream_t st) {
+  const int nb = act8_blocks(C);
+  const int64_t items = static_cast<int64_t>(T) * nb;
+  act8_quantize_kernel<<<grid_of(items), kThreads, 0, st>>>(x, items, nb, C, q, scale);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_act8_dequantize(const int8_t* q, const float* scale, int32_t T, int32_t C,
+                                   int32_t act, mf_bf16* y, cudaStream_t st) {
+  const int nb = act8_blocks(C);
+  const int64_t items = static_cast<int64_t>(T) * nb;
+  const unsigned grid = grid_of(items);
+  if (act == MF_ACT_GELU)
+    act8_dequantize_kernel<MF_ACT_GELU><<<grid, kThreads, 0, st>>>(q, scale, items, nb, C, y);
+  else if (act == MF_ACT_SILU)
+    act8_dequantize_kernel<MF_ACT_SILU><<<grid, kThreads, 0, st>>>(q, scale, items, nb, C, y);
+  else
+    act8_dequantize_kernel<MF_ACT_NONE><<<grid, kThreads, 0, st>>>(q, scale, items, nb, C, y);
+  return cudaGetLastError();
+}
+
+}  // namespace mf

@@ -1,0 +1,1063 @@
+// linear_fused.cu -- the modality-specific linear layer with its epilogue in the
+// product's kernel, and its backward, on sm_100a tensor cores:
+//   z[t] = x[t] W[m]^T + b[m],  out[t] = act(z[t]) + resid[t]
+//   dz = dout * act'(z),  dx[t] = dz[t] W[m],  dW[m] = sum_t dz[t]^T x[t],  db[m] = sum_t dz[t]
+// with m the token's modality (0 image, 1 text), W stored [2][N][K], sums over
+// the modality's tokens. z may be kept for the backward in bf16 or as an 8-bit
+// checkpoint (act8.cu), written by the same epilogue; the backward takes x and z
+// in either form.
+// Source (page title, section): picx.dev "Mage-Flow" summary, Methodology >
+// Native-Resolution MMDiT (each stream keeps its own weights) and > Training
+// Infrastructure (the packed model is trained).
+//
+// One kernel template carries the three products (clusters of two CTAs on two
+// SMs, cta_group::2: 256 x 256 output tiles as M = 256, N = 256 MMAs with fp32
+// accumulators in TMEM, 64 of the inner dimension per stage). Nothing is
+// transposed in memory: the operands are read as they lie, and the tensor core's
+// descriptors say which way they run.
+//   forward  A = x (inner dimension contiguous), B = W (contiguous)
+//   dx       A = dz (contiguous),                B = W (inner dimension strided)
+//   dW       A = dz, B = x (both strided: the inner dimension is the tokens)
+// W has a three-dimensional tensor map (K, N, modality), so a tile past N or K
+// reads zeros and not the other modality's weights. Tails need no padding: rows
+// and columns past the end are read as zeros and not stored.
+//
+// The sum over a modality's tokens walks its runs of consecutive rows (an image,
+// a text) in steps of 64. The last step of a run may reach into rows of the other
+// modality; there the rows past the run are set to zero in shared memory, in both
+// operands, so that an infinity or NaN in a foreign row has no effect. Warps 8..11
+// do that between the copies and the MMAs, and they turn an 8-bit x into bf16.
+//   warp 0      TMA producer (one lane)
+//   warp 1      tcgen05 issuer (one lane of the leader CTA)
+//   warps 4..7  epilogue, one output row per thread, from the accumulator that the
+//               MMAs have left for the other one of the two
+//   warps 8..11 dW only: zero the rows past a run, decode 8-bit x
+// Every wait is bounded.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "act8.cuh"
+#include "gemm_internal.h"
+#include "mf_internal.h"
+#include "mf_ptx.cuh"
+#include "mlp_internal.h"
+
+namespace mf {
+
+namespace {
+
+constexpr int kFwd = 0, kDx = 1, kDw = 2;
+constexpr int kHalf = 128;   // output rows, and B columns, of one CTA of the pair
+constexpr int kTile = 256;   // output tile: rows and columns
+constexpr int kStepK = 64;   // inner dimension per stage: one 128-byte swizzle atom
+constexpr int kBoxBytes = 64 * 64 * 2;  // a 64-column box of 64 rows
+constexpr uint32_t kTmemCols = 512;     // two accumulators of 256 columns
+constexpr int kPrepWarps = 4;
+
+template <int MODE, bool X8>
+struct Layout {
+  static constexpr int A_BYTES = kHalf * kStepK * 2;
+  static constexpr int B_BYTES = kHalf * kStepK * 2;
+  static constexpr int RAW_BYTES = X8 ? kHalf * kStepK : 0;  // int8 codes of x
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + RAW_BYTES;
+  static constexpr int COPY_BYTES = A_BYTES + (X8 ? RAW_BYTES : B_BYTES);  // by TMA, per CTA
+  static constexpr int STAGES = X8 ? 5 : 7;
+  static constexpr int WARPS = MODE == kDw ? 12 : 8;
+  static constexpr int OFF_BAR = STAGES * STAGE_BYTES;
+  // Forward and dx: the leader's FULL counts both CTAs' bytes. dW: each CTA's
+  // copies complete on its own FULL, and READY (the leader's) counts the prep
+  // warps of both. EMPTY and ACC_FULL arrive in both CTAs from the leader's
+  // multicast commits; ACC_EMPTY is the leader's.
+  static constexpr int B_FULL = 0;
+  static constexpr int B_EMPTY = B_FULL + STAGES;
+  static constexpr int B_READY = B_EMPTY + STAGES;
+  static constexpr int B_ACC_FULL = B_READY + (MODE == kDw ? STAGES : 0);
+  static constexpr int B_ACC_EMPTY = B_ACC_FULL + 2;
+  static constexpr int B_DRAIN = B_ACC_EMPTY + 2;
+  static constexpr int NUM_BARS = B_DRAIN + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget of one CTA");
+};
+
+// One (row block, modality) job per entry for the forward and dx.
+struct RowJobs {
+  GemmJobs jobs;
+};
+// The modalities' runs for dW; it0[m][r] = steps before run r.
+struct RunJobs {
+  int32_t n[2];
+  int32_t start[2][MF_MAX_SAMPLES];
+  int32_t len[2][MF_MAX_SAMPLES];
+  int32_t it0[2][MF_MAX_SAMPLES + 1];
+  int32_t units[2];   // output tiles x splits of the modality (0: no tokens)
+  int32_t splits[2];  // parts of the modality's steps
+  float* part;        // [units of split modalities][256][256], or NULL
+};
+
+template <int MODE>
+struct JobsOf {
+  using type = RowJobs;
+};
+template <>
+struct JobsOf<kDw> {
+  using type = RunJobs;
+};
+
+template <int MODE>
+struct Args {
+  typename JobsOf<MODE>::type j;
+  int32_t T, K, N;
+  int32_t n_steps;         // steps of the inner dimension (forward, dx)
+  int32_t col_tiles;       // column tiles of the output
+  int32_t nb;              // column tiles per block of the traversal
+  const uint8_t* tok_mod;
+  const float* x_scale;    // dW with 8-bit x: [T][xnb]
+  int32_t xnb;
+  LinearEpilogue ep;       // forward: all of it; dx and dW: out
+  KernelCtl ctl;
+};
+
+// Unit u -> (row tile or job, column tile): blocks of nb column tiles (the last
+// one may be narrower), inside a block every row in turn. The units in flight
+// share a block's B operand in L2 while A streams past it.
+__device__ __forceinline__ void unit_coords(int u, int rows, int cols, int nb, int& r, int& c) {
+  const int per = rows * nb;
+  const int b = u / per;
+  const int w = min(nb, cols - b * nb);
+  const int i = u - b * per;
+  r = i / w;
+  c = b * nb + (i - r * w);
+}
+
+__device__ __forceinline__ void load_2d(void* dst, const CUtensorMap* map, uint32_t bar, int x,
+                                        int y, bool pair) {
+  if (pair)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+// A box of the weights: modality z of the (K, N, 2) map, completing on the
+// leader's barrier; kept in L2 (evict_last) since every row block reads it.
+__device__ __forceinline__ void load_w(void* dst, const CUtensorMap* map, uint32_t bar, int x,
+                                       int y, int z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t keep_in_l2() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const KernelCtl& ctl,
+                                          volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl, abort_flag));
+}
+
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > limit_ns) return;
+}
+
+// mbar_wait for arrivals from both CTAs that release writes to their shared
+// memory: acquires at cluster scope.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
+                                                  const KernelCtl& ctl, volatile int* abort_flag) {
+  const bool ok = mbar_wait(bar, parity, ctl, abort_flag);
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  return ok;
+}
+
+// What a unit of dW covers: modality, tile, and steps [s0, s1) of its runs.
+struct DwUnit {
+  int m, nt, kt, s0, s1, slot;
+};
+__device__ __forceinline__ DwUnit dw_unit(const Args<kDw>& a, int u) {
+  DwUnit w;
+  w.m = u < a.j.units[0] ? 0 : 1;
+  int i = w.m ? u - a.j.units[0] : u;
+  const int rows = (a.N + kTile - 1) / kTile;
+  const int tiles = rows * a.col_tiles;
+  const int part = i / tiles;
+  i -= part * tiles;
+  unit_coords(i, rows, a.col_tiles, a.nb, w.nt, w.kt);
+  const int total = a.j.it0[w.m][a.j.n[w.m]], p = a.j.splits[w.m];
+  w.s0 = static_cast<int>(static_cast<int64_t>(total) * part / p);
+  w.s1 = static_cast<int>(static_cast<int64_t>(total) * (part + 1) / p);
+  // slots of the image modality's parts come first
+  w.slot = p > 1 ? (w.m == 1 && a.j.splits[0] > 1 ? a.j.units[0] : 0) + part * tiles +
+                       w.nt * a.col_tiles + w.kt
+                 : -1;
+  return w;
+}
+// The walk over a unit's steps: run and first row of the current one.
+struct RunWalk {
+  int r, row, left;
+  __device__ __forceinline__ void start(const Args<kDw>& a, int m, int step) {
+    int lo = 0, hi = a.j.n[m] - 1;  // last run with it0 <= step
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.j.it0[m][mid] <= step) lo = mid; else hi = mid - 1;
+    }
+    r = lo;
+    const int off = (step - a.j.it0[m][r]) * kStepK;
+    row = a.j.start[m][r] + off;
+    left = a.j.len[m][r] - off;
+  }
+  __device__ __forceinline__ void next(const Args<kDw>& a, int m) {
+    row += kStepK;
+    left -= kStepK;
+    if (left <= 0 && r + 1 < a.j.n[m]) {
+      ++r;
+      row = a.j.start[m][r];
+      left = a.j.len[m][r];
+    }
+  }
+};
+
+template <int ACT>
+__device__ __forceinline__ void act32(float (&v)[32]) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e) v[e] = act_fwd<ACT>(v[e]);
+}
+
+// 32 columns of one accumulator row; the caller masks what it stores.
+__device__ __forceinline__ void acc_load32(uint32_t taddr, float (&f)[32]) {
+  uint32_t v[32];
+  tmem_ld32(taddr, v);
+  tmem_ld_wait();
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    asm volatile("" : "+r"(v[e]));
+    f[e] = __uint_as_float(v[e]);
+  }
+}
+
+__device__ __forceinline__ void add_bias32(const float* bias, int left, float (&f)[32]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    if (q * 4 < left) {  // the width is a multiple of 8
+      const float4 b = __ldg(reinterpret_cast<const float4*>(bias) + q);
+      f[4 * q] += b.x;
+      f[4 * q + 1] += b.y;
+      f[4 * q + 2] += b.z;
+      f[4 * q + 3] += b.w;
+    }
+}
+
+__device__ __forceinline__ void store32(mf_bf16* p, int left, const float (&f)[32]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (q * 8 < left) {
+      const uint4 o = make_uint4(pack_bf16x2(f[8 * q], f[8 * q + 1]),
+                                 pack_bf16x2(f[8 * q + 2], f[8 * q + 3]),
+                                 pack_bf16x2(f[8 * q + 4], f[8 * q + 5]),
+                                 pack_bf16x2(f[8 * q + 6], f[8 * q + 7]));
+      __stcs(reinterpret_cast<uint4*>(p) + q, o);
+    }
+}
+
+// The forward's epilogue on one row of a 256-column tile: bias, the kept
+// pre-activation, activation, residual. With an 8-bit checkpoint the row's 128
+// values of a block are read twice from TMEM, once for their largest magnitude;
+// z itself never reaches memory.
+__device__ __forceinline__ void forward_row(const Args<kFwd>& a, uint32_t taddr, int t, int m,
+                                            bool keep, int n0) {
+  const LinearEpilogue& ep = a.ep;
+  const size_t rowoff = static_cast<size_t>(t) * a.N;
+  const float* bias = ep.bias == nullptr ? nullptr : ep.bias + static_cast<size_t>(m) * a.N;
+#pragma unroll 1
+  for (int blk = 0; blk < kTile; blk += kAct8Block) {
+    if (n0 + blk >= a.N) break;
+    float s = 0.f, inv = 0.f;
+    if (ep.z8 != nullptr) {
+      uint32_t top = 0;
+#pragma unroll 1
+      for (int cc = blk; cc < blk + kAct8Block; cc += 32) {
+        const int left = a.N - n0 - cc;
+        if (left <= 0) break;
+        float f[32];
+        acc_load32(taddr + cc, f);
+        if (bias != nullptr) add_bias32(bias + n0 + cc, left, f);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (e < left) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
+      }
+      act8_scale(__uint_as_float(top), s, inv);
+      if (keep)
+        ep.z_scale[static_cast<size_t>(t) * ((a.N + kAct8Block - 1) / kAct8Block) +
+                   (n0 + blk) / kAct8Block] = s;
+    }
+#pragma unroll 1
+    for (int cc = blk; cc < blk + kAct8Block; cc += 32) {
+      const int c0 = n0 + cc, left = a.N - c0;
+      if (left <= 0) break;
+      float f[32];
+      acc_load32(taddr + cc, f);
+      if (bias != nullptr) add_bias32(bias + c0, left, f);
+      if (ep.z8 != nullptr && keep) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q * 8 < left)
+            __stcs(reinterpret_cast<uint2*>(ep.z8 + rowoff + c0) + q,
+                   make_uint2(act8_code4(f + 8 * q, inv), act8_code4(f + 8 * q + 4, inv)));
+      }
+      if (ep.z != nullptr && keep) store32(ep.z + rowoff + c0, left, f);
+      if (ep.act == MF_ACT_GELU) act32<MF_ACT_GELU>(f);
+      if (ep.act == MF_ACT_SILU) act32<MF_ACT_SILU>(f);
+      if (keep) {
+        if (ep.resid != nullptr) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (q * 8 < left) {
+              float r[8];
+              bf16x8_unpack(*(reinterpret_cast<const uint4*>(ep.resid + rowoff + c0) + q), r);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[8 * q + e] += r[e];
+            }
+        }
+        store32(ep.out + rowoff + c0, left, f);
+      }
+    }
+  }
+}
+
+template <int MODE, bool X8>
+__global__ void __launch_bounds__(Layout<MODE, X8>::WARPS * 32, 1)
+    linear_fused_kernel(const __grid_constant__ CUtensorMap map_a,
+                        const __grid_constant__ CUtensorMap map_b,
+                        const __grid_constant__ Args<MODE> args) {
+  using L = Layout<MODE, X8>;
+  constexpr int kStages = L::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::NUM_BARS; ++i) {
+      uint32_t count = 1;
+      if (i == L::B_ACC_EMPTY || i == L::B_ACC_EMPTY + 1) count = 8;  // epilogue warps of the pair
+      if (MODE == kDw && i >= L::B_READY && i < L::B_READY + kStages) count = 2 * kPrepWarps;
+      mbar_init(&bars[i], count);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_map(&map_a);
+    tma_prefetch_map(&map_b);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before either reaches the other's
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int unit0 = static_cast<int>(blockIdx.x >> 1);
+  const int stride = static_cast<int>(gridDim.x >> 1);
+  int units;
+  if constexpr (MODE == kDw)
+    units = args.j.units[0] + args.j.units[1];
+  else
+    units = args.j.jobs.n * args.col_tiles;
+
+  // Row tile, modality and column tile of a unit, and its steps.
+  auto row_job = [&](int u, int& blk, int& m, int& ct) {
+    if constexpr (MODE != kDw) {
+      int ji;
+      unit_coords(u, args.j.jobs.n, args.col_tiles, args.nb, ji, ct);
+      const int job = args.j.jobs.job[ji];
+      blk = job & 0x7fff;
+      m = job >> 15;
+    }
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t keep = keep_in_l2();
+      uint32_t it = 0;
+      bool ok = true;
+      auto stage = [&](uint8_t*& sa, uint32_t& bar) -> bool {
+        const int st = it % kStages;
+        if (!mbar_wait(&bars[L::B_EMPTY + st], ((it / kStages) & 1) ^ 1, args.ctl, abort_flag))
+          return false;
+        sa = smem + st * L::STAGE_BYTES;
+        if constexpr (MODE == kDw) {
+          mbar_expect_tx(&bars[L::B_FULL + st], L::COPY_BYTES);
+          bar = smem_u32(&bars[L::B_FULL + st]);
+        } else {
+          // both CTAs' copies complete on the leader's barrier, which the leader
+          // arms for both (a copy that lands first takes its count below zero)
+          if (rank == 0) mbar_expect_tx(&bars[L::B_FULL + st], 2 * L::COPY_BYTES);
+          bar = cluster_addr(&bars[L::B_FULL + st], 0);
+        }
+        return true;
+      };
+      for (int u = unit0; u < units && ok; u += stride) {
+        uint8_t* sa;
+        uint32_t bar;
+        if constexpr (MODE == kDw) {
+          const DwUnit w = dw_unit(args, u);
+          RunWalk walk;
+          walk.start(args, w.m, w.s0);
+          const int xa = w.nt * kTile + rank * kHalf, xb = w.kt * kTile + rank * kHalf;
+          for (int s = w.s0; s < w.s1; ++s, ++it, walk.next(args, w.m)) {
+            if (!(ok = stage(sa, bar))) break;
+            load_2d(sa, &map_a, bar, xa, walk.row, false);
+            load_2d(sa + kBoxBytes, &map_a, bar, xa + 64, walk.row, false);
+            if constexpr (X8) {
+              load_2d(sa + L::A_BYTES + L::B_BYTES, &map_b, bar, xb, walk.row, false);
+            } else {
+              load_2d(sa + L::A_BYTES, &map_b, bar, xb, walk.row, false);
+              load_2d(sa + L::A_BYTES + kBoxBytes, &map_b, bar, xb + 64, walk.row, false);
+            }
+          }
+        } else {
+          int blk = 0, m = 0, ct = 0;
+          row_job(u, blk, m, ct);
+          const int row = blk * kTile + rank * kHalf, col = ct * kTile + rank * kHalf;
+          for (int s = 0; s < args.n_steps; ++s, ++it) {
+            if (!(ok = stage(sa, bar))) break;
+            load_2d(sa, &map_a, bar, s * kStepK, row, true);
+            if constexpr (MODE == kFwd) {
+              load_w(sa + L::A_BYTES, &map_b, bar, s * kStepK, col, m, keep);
+            } else {
+              load_w(sa + L::A_BYTES, &map_b, bar, col, s * kStepK, m, keep);
+              load_w(sa + L::A_BYTES + kBoxBytes, &map_b, bar, col + 64, s * kStepK, m, keep);
+            }
+          }
+        }
+      }
+      // Every copy this thread started, or whose barrier is this CTA's, lands
+      // before the CTA can exit.
+      if (MODE == kDw || rank == 0)
+        for (int st = 0; st < kStages; ++st)
+          if (it > static_cast<uint32_t>(st)) {
+            const uint32_t last = it - 1 - ((it - 1 - st) % kStages);
+            drain_wait(&bars[L::B_FULL + st], (last / kStages) & 1, args.ctl.wait_limit_ns);
+          }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr int A_MN = MODE == kDw, B_MN = MODE != kFwd;
+      constexpr uint32_t IDESC = idesc_bf16_f32(2 * kHalf, kTile, A_MN, B_MN);
+      // a 16-element step is 32 bytes along a contiguous inner dimension, 16 rows
+      // of 128 bytes along a strided one
+      constexpr uint64_t A_STEP = A_MN ? 128 : 2, B_STEP = B_MN ? 128 : 2;
+      const uint32_t base = smem_u32(smem);
+      const uint64_t a_desc = sdesc_sw128(base, A_MN ? kBoxBytes : 16, 1024);
+      const uint64_t b_desc = sdesc_sw128(base + L::A_BYTES, B_MN ? kBoxBytes : 16, 1024);
+      uint32_t it = 0, ul = 0;
+      bool ok = true;
+      for (int u = unit0; u < units && ok; u += stride, ++ul) {
+        const uint32_t acc = ul & 1;
+        if (!mbar_wait(&bars[L::B_ACC_EMPTY + acc], ((ul >> 1) & 1) ^ 1, args.ctl, abort_flag))
+          break;
+        tc_fence_after();
+        int steps;
+        if constexpr (MODE == kDw) {
+          const DwUnit w = dw_unit(args, u);
+          steps = w.s1 - w.s0;
+        } else {
+          steps = args.n_steps;
+        }
+        const uint32_t d = tmem + acc * kTile;
+        for (int s = 0; s < steps; ++s, ++it) {
+          const int st = it % kStages;
+          if constexpr (MODE == kDw)
+            ok = mbar_wait_cluster(&bars[L::B_READY + st], (it / kStages) & 1, args.ctl, abort_flag);
+          else
+            ok = mbar_wait(&bars[L::B_FULL + st], (it / kStages) & 1, args.ctl, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t so = static_cast<uint64_t>((st * L::STAGE_BYTES) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kStepK / 16; ++kk)
+            umma_ss_pair(d, a_desc + so + kk * A_STEP, b_desc + so + kk * B_STEP, IDESC,
+                         (s > 0 || kk > 0) ? 1u : 0u);
+          umma_commit_pair(&bars[L::B_EMPTY + st], 3);
+        }
+        if (!ok) break;
+        umma_commit_pair(&bars[L::B_ACC_FULL + acc], 3);
+      }
+      // every MMA this thread issued completes before TMEM is released
+      umma_commit_pair(&bars[L::B_DRAIN], 1);
+      drain_wait(&bars[L::B_DRAIN], 0, args.ctl.wait_limit_ns);
+    }
+    __syncwarp();
+  } else if (warp >= 4 && warp < 8) {
+    const int wq = warp & 3;
+    const int row = wq * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+    uint32_t ul = 0;
+    for (int u = unit0; u < units; u += stride, ++ul) {
+      const uint32_t acc = ul & 1;
+      if (!warp_wait(&bars[L::B_ACC_FULL + acc], (ul >> 1) & 1, args.ctl, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + lane_base + acc * kTile;
+      if constexpr (MODE == kDw) {
+        const DwUnit w = dw_unit(args, u);
+        const int n = w.nt * kTile + rank * kHalf + row, k0 = w.kt * kTile;
+        const bool keep = n < args.N;
+        mf_bf16* out = args.ep.out + (static_cast<size_t>(w.m) * args.N + n) * args.K + k0;
+        float* part = w.slot < 0 ? nullptr
+                                 : args.j.part + (static_cast<size_t>(w.slot) * kTile +
+                                                  rank * kHalf + row) * kTile;
+#pragma unroll 1
+        for (int cc = 0; cc < kTile; cc += 32) {
+          const int left = args.K - k0 - cc;
+          if (left <= 0) break;
+          float f[32];
+          acc_load32(taddr + cc, f);
+          if (part != nullptr) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              *(reinterpret_cast<float4*>(part + cc) + q) =
+                  make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+          } else if (keep) {
+            store32(out + cc, left, f);
+          }
+        }
+      } else {
+        int blk = 0, m = 0, ct = 0;
+        row_job(u, blk, m, ct);
+        const int t = blk * kTile + rank * kHalf + row;
+        const bool keep = t < args.T && __ldg(args.tok_mod + t) == m;
+        if constexpr (MODE == kFwd) {
+          forward_row(args, taddr, t, m, keep, ct * kTile);
+        } else {
+          const int k0 = ct * kTile;
+          mf_bf16* out = args.ep.out + static_cast<size_t>(t) * args.K + k0;
+#pragma unroll 1
+          for (int cc = 0; cc < kTile; cc += 32) {
+            const int left = args.K - k0 - cc;
+            if (left <= 0) break;
+            float f[32];
+            acc_load32(taddr + cc, f);
+            if (keep) store32(out + cc, left, f);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars[L::B_ACC_EMPTY + acc], 0));
+    }
+  } else if (MODE == kDw && warp >= 8) {
+    if constexpr (MODE == kDw) {
+      const int tid = threadIdx.x - 8 * 32;
+      uint32_t it = 0;
+      bool ok = true;
+      for (int u = unit0; u < units && ok; u += stride) {
+        const DwUnit w = dw_unit(args, u);
+        RunWalk walk;
+        walk.start(args, w.m, w.s0);
+        for (int s = w.s0; s < w.s1; ++s, ++it, walk.next(args, w.m)) {
+          const int st = it % kStages;
+          const int live = min(walk.left, kStepK);
+          uint8_t* sa = smem + st * L::STAGE_BYTES;
+          float scale = 0.f;
+          if constexpr (X8) {
+            // this thread's row of the step and its 64-column box; a CTA's 128
+            // columns are one block of scales
+            const int kb = (w.kt * kTile + rank * kHalf) / kAct8Block;
+            if ((tid & 63) < live && kb < args.xnb)
+              scale = __ldg(args.x_scale + static_cast<size_t>(walk.row + (tid & 63)) * args.xnb + kb);
+          }
+          if (!(ok = warp_wait(&bars[L::B_FULL + st], (it / kStages) & 1, args.ctl, abort_flag)))
+            break;
+          if constexpr (X8) {
+            // row r of a box is 128 bytes, its 16-byte chunks permuted by r mod 8
+            // (the swizzle); the codes' tile has 128-byte rows swizzled the same way
+            const int r = tid & 63, box = tid >> 6;
+            const uint8_t* codes = sa + L::A_BYTES + L::B_BYTES + r * 128;
+            uint8_t* dst = sa + L::A_BYTES + box * kBoxBytes + r * 128;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint4 q = make_uint4(0, 0, 0, 0);
+              if (r < live) q = *reinterpret_cast<const uint4*>(codes + (((box * 4 + c) ^ (r & 7)) << 4));
+              float f[8];
+              act8_load(make_uint2(q.x, q.y), scale, f);
+              *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (r & 7)) << 4)) = bf16x8_pack(f);
+              act8_load(make_uint2(q.z, q.w), scale, f);
+              *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (r & 7)) << 4)) = bf16x8_pack(f);
+            }
+          }
+          if (live < kStepK) {
+            // rows past the run: A, and B where no decoding has left zeros there
+            const int boxes = X8 ? 2 : 4;
+            for (int i = tid; i < boxes * (kStepK - live) * 8; i += kPrepWarps * 32) {
+              const int b = i / ((kStepK - live) * 8), o = i - b * (kStepK - live) * 8;
+              *reinterpret_cast<uint4*>(sa + b * kBoxBytes + live * 128 + o * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+          }
+          // this thread's writes before the tensor core's reads
+          if (X8 || live < kStepK) fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars[L::B_READY + st], 0));
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // Neither CTA frees TMEM or leaves before both are here: the leader's MMAs write
+  // both CTAs' TMEM, and copies and arrivals cross between them.
+  cluster_sync();
+  if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+// dW[m] = the sum of its parts, in order, rounded once. One thread per 8 columns.
+__global__ void __launch_bounds__(256) dw_parts_kernel(const float* __restrict__ part, int splits,
+                                                       int N, int K, int col_tiles, int tiles,
+                                                       mf_bf16* __restrict__ dW) {
+  const int groups = K / 8;
+  const int64_t total = static_cast<int64_t>(N) * groups;
+  const int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+  if (i < total) {
+    const int n = static_cast<int>(i / groups), k = static_cast<int>(i - static_cast<int64_t>(n) * groups) * 8;
+    const float* p = part + ((static_cast<size_t>(n / kTile) * col_tiles + k / kTile) * kTile +
+                             n % kTile) * kTile + k % kTile;
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < splits; ++s, p += static_cast<size_t>(tiles) * kTile * kTile) {
+      const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
+      const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+      f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
+      f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
+    }
+    *reinterpret_cast<uint4*>(dW + static_cast<size_t>(n) * K + k) = bf16x8_pack(f);
+  }
+}
+
+// ------------------------------------------------------------ dz and db
+// dz = dout act'(z) (bf16, the operand of both products) and the modality sums of
+// the unrounded dz. A CTA takes kDzRows rows of 256 channels: 32 lanes of eight
+// channels by eight row lanes, four rows of loads in flight per thread; the row
+// lanes' sums meet in shared memory and leave as part[chunk][modality][N], which
+// dz_cols_kernel adds in order. HBM-bound. ACT none: only the sums.
+constexpr int kDzRows = 128;
+constexpr int kDzUnroll = 4;
+
+template <int ACT, bool Z8>
+__global__ void __launch_bounds__(256) dz_kernel(const mf_bf16* __restrict__ dout,
+                                                 const mf_bf16* __restrict__ z, const Act8 z8,
+                                                 const uint8_t* __restrict__ tok_mod, int T, int N,
+                                                 mf_bf16* __restrict__ dz, float* __restrict__ part,
+                                                 KernelCtl ctl) {
+  __shared__ float acc[2][8][256];
+  const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
+  const int c = blockIdx.y * 256 + cl * 8;
+  const bool on = c < N;
+  const int nb = (N + kAct8Block - 1) / kAct8Block;
+  const int r0 = blockIdx.x * kDzRows, r1 = min(T, r0 + kDzRows);
+  float sum[2][8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[0][e] = sum[1][e] = 0.f;
+  for (int t0 = r0 + rl; t0 < r1; t0 += 8 * kDzUnroll) {
+    uint4 vd[kDzUnroll], vz[kDzUnroll];
+    float vs[kDzUnroll];
+    int mod[kDzUnroll];
+#pragma unroll
+    for (int u = 0; u < kDzUnroll; ++u) {
+      const int t = t0 + u * 8;
+      const bool live = t < r1 && on;
+      const size_t off = static_cast<size_t>(t) * N + c;
+      mod[u] = live ? __ldg(tok_mod + t) : 2;
+      vd[u] = live ? __ldg(reinterpret_cast<const uint4*>(dout + off)) : make_uint4(0, 0, 0, 0);
+      vz[u] = make_uint4(0, 0, 0, 0);
+      vs[u] = 0.f;
+      if (ACT != MF_ACT_NONE && live) {
+        if constexpr (Z8) {
+          const uint2 q = __ldcs(reinterpret_cast<const uint2*>(z8.q + off));
+          vz[u].x = q.x;
+          vz[u].y = q.y;
+          vs[u] = __ldg(z8.scale + static_cast<size_t>(t) * nb + c / kAct8Block);
+        } else {
+          vz[u] = __ldcs(reinterpret_cast<const uint4*>(z + off));
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kDzUnroll; ++u) {
+      const int t = t0 + u * 8;
+      if (t >= r1 || !on) continue;
+      float d[8];
+      bf16x8_unpack(vd[u], d);
+      if constexpr (ACT != MF_ACT_NONE) {
+        float f[8];
+        if constexpr (Z8)
+          act8_load(make_uint2(vz[u].x, vz[u].y), vs[u], f);
+        else
+          bf16x8_unpack(vz[u], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[e] *= act_grad<ACT>(f[e]);
+        *reinterpret_cast<uint4*>(dz + static_cast<size_t>(t) * N + c) = bf16x8_pack(d);
+      }
+      if (mod[u] > 1) {
+        atomicCAS(ctl.err, 0, static_cast<int>(MF_ERR_INVALID));
+        continue;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sum[0][e] += mod[u] == 0 ? d[e] : 0.f;
+        sum[1][e] += mod[u] == 1 ? d[e] : 0.f;
+      }
+    }
+  }
+  if (part == nullptr) return;
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[m][rl][cl * 8 + e] = sum[m][e];
+  __syncthreads();
+  const int col = blockIdx.y * 256 + threadIdx.x;
+  if (col < N) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      float v = 0.f;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) v += acc[m][r][threadIdx.x];
+      part[(static_cast<size_t>(blockIdx.x) * 2 + m) * N + col] = v;
+    }
+  }
+}
+
+// db = the sum of the chunks' partials in order; 32 columns x 8 slices per CTA.
+__global__ void __launch_bounds__(256) dz_cols_kernel(const float* __restrict__ part, int chunks,
+                                                      int cols, float* __restrict__ db) {
+  __shared__ float s[8][32];
+  const int col = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
+  float v = 0.f;
+  if (col < cols) {
+#pragma unroll 4
+    for (int k = slice; k < chunks; k += 8) v += __ldg(part + static_cast<size_t>(k) * cols + col);
+  }
+  s[slice][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (slice == 0 && col < cols) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) v += s[k][threadIdx.x & 31];
+    db[col] = v;
+  }
+}
+
+// ------------------------------------------------------------ host side
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+                       cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<EncodeTiledFn>(p)
+               : nullptr;
+  }();
+  return fn;
+}
+
+// [sets][rows][cols] with boxes of box_cols x box_rows, 128-byte swizzle; what
+// lies outside reads as zeros. sets 0: a two-dimensional map.
+bool make_map(CUtensorMap* map, const void* base, bool bytes, int64_t cols, int64_t rows, int sets,
+              int box_cols, int box_rows) {
+  const EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  const int64_t esize = bytes ? 1 : 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(sets)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols * esize),
+                                 static_cast<cuuint64_t>(cols * rows * esize)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+             sets > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, bool X8>
+cudaLaunchConfig_t config(int clusters, cudaLaunchAttribute* attr, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * clusters);
+  cfg.blockDim = dim3(Layout<MODE, X8>::WARPS * 32);
+  cfg.dynamicSmemBytes = Layout<MODE, X8>::SMEM_BYTES;
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Clusters of two that can be resident at once; 0 if the kernel cannot run.
+template <int MODE, bool X8>
+int max_clusters() {
+  static int cached[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (cached[dev] == 0) {
+    if (cudaFuncSetAttribute(linear_fused_kernel<MODE, X8>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Layout<MODE, X8>::SMEM_BYTES) != cudaSuccess)
+      return 0;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config<MODE, X8>(1, attr, nullptr);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, linear_fused_kernel<MODE, X8>, &cfg) != cudaSuccess)
+      return 0;
+    cached[dev] = n;
+  }
+  return cached[dev];
+}
+
+template <int MODE, bool X8>
+cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const Args<MODE>& a,
+                           int units, cudaStream_t st) {
+  const int mc = max_clusters<MODE, X8>();
+  if (mc <= 0) return cudaErrorInvalidConfiguration;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = config<MODE, X8>(units < mc ? units : mc, attr, st);
+  return cudaLaunchKernelEx(&cfg, linear_fused_kernel<MODE, X8>, ma, mb, a);
+}
+
+int tiles_of(int64_t v) { return static_cast<int>((v + kTile - 1) / kTile); }
+
+// Row blocks of kTile rows and the modalities each holds; T <= kMaxGemmTiles * 128.
+void row_jobs(const TokenRuns& runs, int32_t T, GemmJobs* jobs) {
+  static thread_local uint8_t has[kMaxGemmTiles];
+  const int tiles = tiles_of(T);
+  memset(has, 0, static_cast<size_t>(tiles));
+  for (int m = 0; m < 2; ++m)
+    for (int r = 0; r < runs.n[m]; ++r)
+      for (int b = runs.start[m][r] / kTile; b <= (runs.start[m][r] + runs.len[m][r] - 1) / kTile; ++b)
+        has[b] |= 1u << m;
+  jobs->n = 0;
+  for (int b = 0; b < tiles; ++b)
+    for (int m = 0; m < 2; ++m)
+      if (has[b] & (1u << m)) jobs->job[jobs->n++] = static_cast<uint16_t>(b | (m << 15));
+}
+
+template <int MODE>
+void fill(Args<MODE>& a, int32_t T, int32_t K, int32_t N, int cols, const KernelCtl& ctl) {
+  a.T = T;
+  a.K = K;
+  a.N = N;
+  a.col_tiles = tiles_of(cols);
+  a.nb = a.col_tiles < 12 ? a.col_tiles : 12;
+  a.ctl = ctl;
+}
+
+// Pairs of SMs on a B200 (148 SMs): what dW's split and its workspace are sized by.
+constexpr int kPairs = 74;
+
+// Parts of a modality's steps: one, unless its tiles leave more than half of the
+// pairs without work; then as many as fill them, of at least four steps each.
+int dw_splits(int tiles, int steps) {
+  const int by_pairs = kPairs / tiles, by_steps = steps / 4;
+  const int p = by_pairs < by_steps ? by_pairs : by_steps;
+  return p > 1 ? p : 1;
+}
+
+size_t round256(size_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+
+bool token_runs(const mf_sample_desc* desc, int32_t S, TokenRuns* runs, int32_t* T) {
+  memset(runs->n, 0, sizeof(runs->n));
+  memset(runs->count, 0, sizeof(runs->count));
+  int64_t row = 0;
+  for (int32_t s = 0; s < S; ++s) {
+    const mf_sample_desc& d = desc[s];
+    if (d.frames < 0 || d.grid_h < 0 || d.grid_w < 0 || d.n_text < 0 || d.grid_h > MF_MAX_TOKENS ||
+        d.grid_w > MF_MAX_TOKENS || d.frames > MF_MAX_TOKENS)
+      return false;
+    const int64_t plane = static_cast<int64_t>(d.grid_h) * d.grid_w;
+    if (plane > MF_MAX_TOKENS) return false;
+    const int64_t n[2] = {d.frames * plane, d.n_text};
+    for (int m = 0; m < 2; ++m) {
+      if (row + n[m] > MF_MAX_TOKENS) return false;
+      if (n[m] == 0) continue;
+      const int r = runs->n[m];
+      if (r > 0 && runs->start[m][r - 1] + runs->len[m][r - 1] == row) {
+        runs->len[m][r - 1] += static_cast<int32_t>(n[m]);
+      } else {
+        runs->start[m][r] = static_cast<int32_t>(row);
+        runs->len[m][r] = static_cast<int32_t>(n[m]);
+        runs->n[m] = r + 1;
+      }
+      runs->count[m] += static_cast<int32_t>(n[m]);
+      row += n[m];
+    }
+  }
+  *T = static_cast<int32_t>(row);
+  return true;
+}
+
+cudaError_t launch_linear_fused(const mf_bf16* x, const mf_bf16* W, const TokenRuns& runs,
+                                const uint8_t* tok_mod, int32_t T, int32_t K, int32_t N,
+                                const LinearEpilogue& ep, const KernelCtl& ctl, cudaStream_t st) {
+  CUtensorMap ma, mb;
+  if (!make_map(&ma, x, false, K, T, 0, kStepK, kHalf) ||
+      !make_map(&mb, W, false, K, N, 2, kStepK, kHalf))
+    return cudaErrorInvalidValue;
+  static thread_local Args<kFwd> a;
+  fill(a, T, K, N, N, ctl);
+  row_jobs(runs, T, &a.j.jobs);
+  a.n_steps = (K + kStepK - 1) / kStepK;
+  a.tok_mod = tok_mod;
+  a.ep = ep;
+  return launch_product<kFwd, false>(ma, mb, a, a.j.jobs.n * a.col_tiles, st);
+}
+
+// Workspace, in this order: dz [T][N] bf16; db's partials; x in bf16 (an 8-bit x
+// whose rows TMA cannot address); dW's parts.
+size_t linear_fused_bwd_ws(int32_t T, int32_t K, int32_t N) {
+  const size_t chunks = static_cast<size_t>((T + kDzRows - 1) / kDzRows);
+  const int tiles = tiles_of(N) * tiles_of(K);
+  const size_t parts = tiles * 2 <= kPairs ? static_cast<size_t>(2) * kPairs : 0;
+  return round256(static_cast<size_t>(T) * N * 2) + round256(chunks * 2 * N * sizeof(float)) +
+         (K % 16 != 0 ? round256(static_cast<size_t>(T) * K * 2) : 0) +
+         parts * kTile * kTile * sizeof(float);
+}
+
+cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, int32_t T, int32_t K,
+                                    int32_t N, void* ws, const KernelCtl& ctl, cudaStream_t st) {
+  uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+  mf_bf16* dz_ws = reinterpret_cast<mf_bf16*>(w);
+  w += round256(static_cast<size_t>(T) * N * 2);
+  const int chunks = (T + kDzRows - 1) / kDzRows;
+  float* part = reinterpret_cast<float*>(w);
+  w += round256(static_cast<size_t>(chunks) * 2 * N * sizeof(float));
+  mf_bf16* x_ws = reinterpret_cast<mf_bf16*>(w);
+  if (K % 16 != 0) w += round256(static_cast<size_t>(T) * K * 2);
+  float* dw_part = reinterpret_cast<float*>(w);
+  cudaError_t e;
+
+  const mf_bf16* dz = b.act == MF_ACT_NONE ? b.dout : dz_ws;
+  if (b.act != MF_ACT_NONE || b.db != nullptr) {
+    const dim3 grid(chunks, (N + 255) / 256);
+    float* p = b.db != nullptr ? part : nullptr;
+#define MF_DZ(ACT, Z8) \
+  dz_kernel<ACT, Z8><<<grid, 256, 0, st>>>(b.dout, b.z, b.z8, b.tok_mod, T, N, dz_ws, p, ctl)
+    if (b.act == MF_ACT_NONE) MF_DZ(MF_ACT_NONE, false);
+    else if (b.act == MF_ACT_GELU && b.z8.q != nullptr) MF_DZ(MF_ACT_GELU, true);
+    else if (b.act == MF_ACT_GELU) MF_DZ(MF_ACT_GELU, false);
+    else if (b.z8.q != nullptr) MF_DZ(MF_ACT_SILU, true);
+    else MF_DZ(MF_ACT_SILU, false);
+#undef MF_DZ
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (b.db != nullptr) {
+      dz_cols_kernel<<<(2 * N + 31) / 32, 256, 0, st>>>(part, chunks, 2 * N, b.db);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+  }
+
+  if (b.dx != nullptr) {
+    CUtensorMap ma, mb;
+    if (!make_map(&ma, dz, false, N, T, 0, kStepK, kHalf) ||
+        !make_map(&mb, b.W, false, K, N, 2, 64, kStepK))
+      return cudaErrorInvalidValue;
+    static thread_local Args<kDx> a;
+    fill(a, T, K, N, K, ctl);
+    row_jobs(runs, T, &a.j.jobs);
+    a.n_steps = (N + kStepK - 1) / kStepK;
+    a.tok_mod = b.tok_mod;
+    a.ep = LinearEpilogue{};
+    a.ep.out = b.dx;
+    e = launch_product<kDx, false>(ma, mb, a, a.j.jobs.n * a.col_tiles, st);
+    if (e != cudaSuccess) return e;
+  }
+
+  if (b.dW != nullptr) {
+    // TMA rows of 8-bit codes need a width that is a multiple of 16
+    const bool direct8 = b.x == nullptr && K % 16 == 0;
+    const mf_bf16* x = b.x;
+    if (b.x == nullptr && !direct8) {
+      if ((e = launch_act8_dequantize(b.x8.q, b.x8.scale, T, K, MF_ACT_NONE, x_ws, st)) != cudaSuccess)
+        return e;
+      x = x_ws;
+    }
+    CUtensorMap ma, mb;
+    if (!make_map(&ma, dz, false, N, T, 0, 64, kStepK) ||
+        !(direct8 ? make_map(&mb, b.x8.q, true, K, T, 0, kHalf, kStepK)
+                  : make_map(&mb, x, false, K, T, 0, 64, kStepK)))
+      return cudaErrorInvalidValue;
+    static thread_local Args<kDw> a;
+    fill(a, T, K, N, K, ctl);
+    a.ep = LinearEpilogue{};
+    a.ep.out = b.dW;
+    a.x_scale = b.x8.scale;
+    a.xnb = act8_blocks(K);
+    a.j.part = dw_part;
+    const int tiles = tiles_of(N) * a.col_tiles;
+    for (int m = 0; m < 2; ++m) {
+      a.j.n[m] = runs.n[m];
+      a.j.it0[m][0] = 0;
+      for (int r = 0; r < runs.n[m]; ++r) {
+        a.j.start[m][r] = runs.start[m][r];
+        a.j.len[m][r] = runs.len[m][r];
+        a.j.it0[m][r + 1] = a.j.it0[m][r] + (runs.len[m][r] + kStepK - 1) / kStepK;
+      }
+      if (runs.count[m] == 0) {
+        const size_t bytes = static_cast<size_t>(N) * K * 2;
+        if ((e = cudaMemsetAsync(reinterpret_cast<uint8_t*>(b.dW) + m * bytes, 0, bytes, st)) !=
+            cudaSuccess)
+          return e;
+        a.j.splits[m] = 1;
+        a.j.units[m] = 0;
+        continue;
+      }
+      a.j.splits[m] = dw_splits(tiles, a.j.it0[m][runs.n[m]]);
+      a.j.units[m] = tiles * a.j.splits[m];
+    }
+    const int units = a.j.units[0] + a.j.units[1];
+    e = direct8 ? launch_product<kDw, true>(ma, mb, a, units, st)
+                : launch_product<kDw, false>(ma, mb, a, units, st);
+    if (e != cudaSuccess) return e;
+    float* part = dw_part;
+    for (int m = 0; m < 2; ++m) {
+      if (a.j.splits[m] == 1) continue;
+      const int64_t groups = static_cast<int64_t>(N) * (K / 8);
+      dw_parts_kernel<<<static_cast<unsigned>((groups + 255) / 256), 256, 0, st>>>(
+          part, a.j.splits[m], N, K, a.col_tiles, tiles, b.dW + static_cast<size_t>(m) * N * K);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      part += static_cast<size_t>(a.j.units[m]) * kTile * kTile;
+    }
+  }
+  return cudaSuccess;
+}
+
+}  // namespace mf

@@ -14,6 +14,7 @@
 #include "cfg_internal.h"
 #include "gemm_internal.h"
 #include "mf_internal.h"
+#include "mlp_internal.h"
 #include "vae_internal.h"
 
 namespace mf {
@@ -639,6 +640,230 @@ mf_status mf_modality_linear(const mf_bf16* x, const mf_bf16* W, const uint8_t* 
     return MF_ERR_UNSUPPORTED;
   return cuda_status(launch_modality_linear(x, W, tok_mod, jobs, pair, static_cast<int32_t>(T), K,
                                             N, act, out, ctl, stream));
+}
+
+namespace {
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+// Every non-NULL output is clear of every input and of the other outputs.
+bool outputs_clear(const Range* outs, int n_out, const Range* ins, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    if (outs[i].p == nullptr) continue;
+    for (int j = 0; j < n_in; ++j)
+      if (ins[j].p != nullptr && overlap(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes))
+        return false;
+    for (int j = i + 1; j < n_out; ++j)
+      if (outs[j].p != nullptr && overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+        return false;
+  }
+  return true;
+}
+
+constexpr int32_t kMaxWidth = 1 << 20;    // channels of an activation or a linear layer
+constexpr int32_t kMaxNormWidth = 8192;   // channels of a layer-norm row
+constexpr int32_t kMaxLinearTokens = kMaxGemmTiles * 128;
+
+bool known_act(int32_t act) {
+  return act == MF_ACT_NONE || act == MF_ACT_GELU || act == MF_ACT_SILU;
+}
+size_t act8_scale_bytes(int64_t T, int32_t C) {
+  return static_cast<size_t>(T) * act8_blocks(C) * 4;
+}
+}  // namespace
+
+mf_status mf_act8_quantize(const mf_bf16* x, int32_t T, int32_t C, int8_t* q, float* scale,
+                           cudaStream_t stream) {
+  if (T < 0 || T > MF_MAX_TOKENS || C < 8 || C % 8 != 0 || C > kMaxWidth) return MF_ERR_INVALID;
+  if (T == 0) return MF_OK;
+  if (x == nullptr || q == nullptr || scale == nullptr || !aligned16(x) || !aligned16(q) ||
+      !aligned16(scale))
+    return MF_ERR_INVALID;
+  const size_t n = static_cast<size_t>(T) * C;
+  const Range in[] = {{x, 2 * n}}, out[] = {{q, n}, {scale, act8_scale_bytes(T, C)}};
+  if (!outputs_clear(out, 2, in, 1)) return MF_ERR_INVALID;
+  return cuda_status(launch_act8_quantize(x, T, C, q, scale, stream));
+}
+
+mf_status mf_act8_dequantize(const int8_t* q, const float* scale, int32_t T, int32_t C,
+                             int32_t act, mf_bf16* y, cudaStream_t stream) {
+  if (T < 0 || T > MF_MAX_TOKENS || C < 8 || C % 8 != 0 || C > kMaxWidth || !known_act(act))
+    return MF_ERR_INVALID;
+  if (T == 0) return MF_OK;
+  if (q == nullptr || scale == nullptr || y == nullptr || !aligned16(q) || !aligned16(scale) ||
+      !aligned16(y))
+    return MF_ERR_INVALID;
+  const size_t n = static_cast<size_t>(T) * C;
+  const Range in[] = {{q, n}, {scale, act8_scale_bytes(T, C)}}, out[] = {{y, 2 * n}};
+  if (!outputs_clear(out, 1, in, 2)) return MF_ERR_INVALID;
+  return cuda_status(launch_act8_dequantize(q, scale, T, C, act, y, stream));
+}
+
+mf_status mf_layer_norm(const mf_bf16* x, const float* gamma, const float* beta,
+                        const uint8_t* tok_mod, int32_t T, int32_t hid, float eps, mf_bf16* y,
+                        float* stats, cudaStream_t stream) {
+  if (T < 0 || T > MF_MAX_TOKENS || hid < 8 || hid % 8 != 0 || !(eps >= 0.f) || !std::isfinite(eps))
+    return MF_ERR_INVALID;
+  if (hid > kMaxNormWidth) return MF_ERR_UNSUPPORTED;
+  if (T == 0) return MF_OK;
+  if (x == nullptr || gamma == nullptr || beta == nullptr || tok_mod == nullptr || y == nullptr ||
+      !aligned16(x) || !aligned16(gamma) || !aligned16(beta) || !aligned16(y) || !aligned16(stats))
+    return MF_ERR_INVALID;
+  const size_t row = static_cast<size_t>(T) * hid * 2, par = static_cast<size_t>(hid) * 8;
+  const Range in[] = {{x, row}, {gamma, par}, {beta, par}, {tok_mod, static_cast<size_t>(T)}};
+  const Range out[] = {{y, row}, {stats, static_cast<size_t>(T) * 8}};
+  if (!outputs_clear(out, 2, in, 4)) return MF_ERR_INVALID;
+  KernelCtl ctl;
+  if (cudaError_t ge = get_ctl(&ctl); ge != cudaSuccess) return cuda_status(ge);
+  return cuda_status(launch_layer_norm(x, gamma, beta, tok_mod, T, hid, eps, y, stats, ctl, stream));
+}
+
+size_t mf_layer_norm_bwd_workspace_size(int32_t T, int32_t hid) {
+  if (T < 1 || hid < 8 || hid % 8 != 0 || hid > kMaxNormWidth) return 0;
+  return layer_norm_bwd_ws(T, hid) + 256;
+}
+
+mf_status mf_layer_norm_bwd(const mf_bf16* dy, const mf_bf16* x, const int8_t* x8,
+                            const float* x_scale, const float* gamma, const float* stats,
+                            const uint8_t* tok_mod, const mf_bf16* resid, int32_t T, int32_t hid,
+                            mf_bf16* dx, float* dgamma, float* dbeta, void* workspace,
+                            size_t ws_bytes, cudaStream_t stream) {
+  if (T < 0 || T > MF_MAX_TOKENS || hid < 8 || hid % 8 != 0) return MF_ERR_INVALID;
+  if (hid > kMaxNormWidth) return MF_ERR_UNSUPPORTED;
+  if (dgamma == nullptr || dbeta == nullptr || !aligned16(dgamma) || !aligned16(dbeta))
+    return MF_ERR_INVALID;
+  const size_t par = static_cast<size_t>(hid) * 8;
+  if (overlap(dgamma, par, dbeta, par)) return MF_ERR_INVALID;
+  if (T == 0) {
+    if (cudaError_t e = cudaMemsetAsync(dgamma, 0, par, stream); e != cudaSuccess) return cuda_status(e);
+    return cuda_status(cudaMemsetAsync(dbeta, 0, par, stream));
+  }
+  // the input as bf16 or as a checkpoint, not both
+  if ((x == nullptr) == (x8 == nullptr) || (x8 == nullptr) != (x_scale == nullptr) ||
+      dy == nullptr || gamma == nullptr || stats == nullptr || tok_mod == nullptr ||
+      dx == nullptr || workspace == nullptr)
+    return MF_ERR_INVALID;
+  for (const void* p : {static_cast<const void*>(dy), static_cast<const void*>(x),
+                        static_cast<const void*>(x8), static_cast<const void*>(x_scale),
+                        static_cast<const void*>(gamma), static_cast<const void*>(stats),
+                        static_cast<const void*>(resid), static_cast<const void*>(dx),
+                        static_cast<const void*>(workspace)})
+    if (!aligned16(p)) return MF_ERR_INVALID;
+  const size_t ws = mf_layer_norm_bwd_workspace_size(T, hid);
+  if (ws_bytes < ws) return MF_ERR_INVALID;
+  const size_t n = static_cast<size_t>(T) * hid;
+  if (resid != nullptr && dx != resid && overlap(dx, 2 * n, resid, 2 * n)) return MF_ERR_INVALID;
+  const Range in[] = {{dy, 2 * n},          {x, 2 * n},     {x8, n},
+                      {x_scale, act8_scale_bytes(T, hid)}, {gamma, par},
+                      {stats, static_cast<size_t>(T) * 8}, {tok_mod, static_cast<size_t>(T)},
+                      {dx == resid ? nullptr : resid, 2 * n}};
+  const Range out[] = {{dx, 2 * n}, {dgamma, par}, {dbeta, par}, {workspace, ws}};
+  if (!outputs_clear(out, 4, in, 8)) return MF_ERR_INVALID;
+  KernelCtl ctl;
+  if (cudaError_t ge = get_ctl(&ctl); ge != cudaSuccess) return cuda_status(ge);
+  void* w0 = reinterpret_cast<void*>(round_up(reinterpret_cast<uintptr_t>(workspace), 256));
+  return cuda_status(launch_layer_norm_bwd(dy, x, Act8{x8, x_scale}, gamma, stats, tok_mod, resid,
+                                           T, hid, dx, dgamma, dbeta, w0, ctl, stream));
+}
+
+mf_status mf_linear_fused(const mf_bf16* x, const mf_bf16* W, const float* bias,
+                          const mf_bf16* resid, const uint8_t* tok_mod,
+                          const mf_sample_desc* desc, int32_t S, int32_t K, int32_t N, int32_t act,
+                          mf_bf16* z, int8_t* z8, float* z_scale, mf_bf16* out,
+                          cudaStream_t stream) {
+  if (desc == nullptr || S < 1 || S > MF_MAX_SAMPLES || K < 8 || K % 8 != 0 || K > kMaxWidth ||
+      N < 8 || N % 8 != 0 || N > kMaxWidth || !known_act(act))
+    return MF_ERR_INVALID;
+  static thread_local TokenRuns runs;
+  int32_t T = 0;
+  if (!token_runs(desc, S, &runs, &T)) return MF_ERR_INVALID;
+  if (T > kMaxLinearTokens) return MF_ERR_UNSUPPORTED;
+  if (T == 0) return MF_OK;
+  if (x == nullptr || W == nullptr || tok_mod == nullptr || out == nullptr ||
+      (z8 == nullptr) != (z_scale == nullptr))
+    return MF_ERR_INVALID;
+  for (const void* p : {static_cast<const void*>(x), static_cast<const void*>(W),
+                        static_cast<const void*>(bias), static_cast<const void*>(resid),
+                        static_cast<const void*>(z), static_cast<const void*>(z8),
+                        static_cast<const void*>(z_scale), static_cast<const void*>(out)})
+    if (!aligned16(p)) return MF_ERR_INVALID;
+  const size_t xb = static_cast<size_t>(T) * K * 2, ob = static_cast<size_t>(T) * N * 2;
+  if (resid != nullptr && resid != out && overlap(resid, ob, out, ob)) return MF_ERR_INVALID;
+  const Range in[] = {{x, xb},
+                      {W, static_cast<size_t>(N) * K * 4},
+                      {bias, static_cast<size_t>(N) * 8},
+                      {tok_mod, static_cast<size_t>(T)}};
+  const Range outs[] = {{out, ob}, {z, ob}, {z8, ob / 2}, {z_scale, act8_scale_bytes(T, N)}};
+  if (!outputs_clear(outs, 4, in, 4)) return MF_ERR_INVALID;
+  if (resid != nullptr && resid != out) {
+    const Range r[] = {{resid, ob}};
+    if (!outputs_clear(outs, 4, r, 1)) return MF_ERR_INVALID;
+  }
+  KernelCtl ctl;
+  if (cudaError_t ge = get_ctl(&ctl); ge != cudaSuccess) return cuda_status(ge);
+  const LinearEpilogue ep{bias, resid, z, z8, z_scale, out, act};
+  return cuda_status(launch_linear_fused(x, W, runs, tok_mod, T, K, N, ep, ctl, stream));
+}
+
+size_t mf_linear_fused_bwd_workspace_size(int32_t T, int32_t K, int32_t N) {
+  if (T < 1 || T > MF_MAX_TOKENS || K < 8 || K % 8 != 0 || K > kMaxWidth || N < 8 || N % 8 != 0 ||
+      N > kMaxWidth)
+    return 0;
+  return linear_fused_bwd_ws(T, K, N) + 256;
+}
+
+mf_status mf_linear_fused_bwd(const mf_bf16* dout, const mf_bf16* x, const int8_t* x8,
+                              const float* x_scale, const mf_bf16* W, const mf_bf16* z,
+                              const int8_t* z8, const float* z_scale, const uint8_t* tok_mod,
+                              const mf_sample_desc* desc, int32_t S, int32_t K, int32_t N,
+                              int32_t act, mf_bf16* dx, mf_bf16* dW, float* db, void* workspace,
+                              size_t ws_bytes, cudaStream_t stream) {
+  if (desc == nullptr || S < 1 || S > MF_MAX_SAMPLES || K < 8 || K % 8 != 0 || K > kMaxWidth ||
+      N < 8 || N % 8 != 0 || N > kMaxWidth || !known_act(act) ||
+      (dx == nullptr && dW == nullptr && db == nullptr))
+    return MF_ERR_INVALID;
+  static thread_local TokenRuns runs;
+  int32_t T = 0;
+  if (!token_runs(desc, S, &runs, &T)) return MF_ERR_INVALID;
+  if (T > kMaxLinearTokens) return MF_ERR_UNSUPPORTED;
+  const size_t wb = static_cast<size_t>(N) * K * 4, bb = static_cast<size_t>(N) * 8;
+  if (!aligned16(dx) || !aligned16(dW) || !aligned16(db)) return MF_ERR_INVALID;
+  if (dW != nullptr && db != nullptr && overlap(dW, wb, db, bb)) return MF_ERR_INVALID;
+  if (T == 0) {  // sums over no tokens
+    cudaError_t e = cudaSuccess;
+    if (dW != nullptr) e = cudaMemsetAsync(dW, 0, wb, stream);
+    if (e == cudaSuccess && db != nullptr) e = cudaMemsetAsync(db, 0, bb, stream);
+    return cuda_status(e);
+  }
+  if (dout == nullptr || tok_mod == nullptr || workspace == nullptr ||
+      (x8 == nullptr) != (x_scale == nullptr) || (z8 == nullptr) != (z_scale == nullptr) ||
+      (dx != nullptr && W == nullptr))
+    return MF_ERR_INVALID;
+  // dW needs the input, act' the pre-activation: each in one form, not both
+  if (dW != nullptr && (x == nullptr) == (x8 == nullptr)) return MF_ERR_INVALID;
+  if (act != MF_ACT_NONE && (z == nullptr) == (z8 == nullptr)) return MF_ERR_INVALID;
+  for (const void* p : {static_cast<const void*>(dout), static_cast<const void*>(x),
+                        static_cast<const void*>(x8), static_cast<const void*>(x_scale),
+                        static_cast<const void*>(W), static_cast<const void*>(z),
+                        static_cast<const void*>(z8), static_cast<const void*>(z_scale),
+                        static_cast<const void*>(workspace)})
+    if (!aligned16(p)) return MF_ERR_INVALID;
+  const size_t ws = mf_linear_fused_bwd_workspace_size(T, K, N);
+  if (ws_bytes < ws) return MF_ERR_INVALID;
+  const size_t nx = static_cast<size_t>(T) * K, nz = static_cast<size_t>(T) * N;
+  const Range in[] = {{dout, 2 * nz}, {x, 2 * nx}, {x8, nx}, {x_scale, act8_scale_bytes(T, K)},
+                      {W, wb},        {z, 2 * nz}, {z8, nz}, {z_scale, act8_scale_bytes(T, N)},
+                      {tok_mod, static_cast<size_t>(T)}};
+  const Range outs[] = {{dx, 2 * nx}, {dW, wb}, {db, bb}, {workspace, ws}};
+  if (!outputs_clear(outs, 4, in, 9)) return MF_ERR_INVALID;
+  KernelCtl ctl;
+  if (cudaError_t ge = get_ctl(&ctl); ge != cudaSuccess) return cuda_status(ge);
+  void* w0 = reinterpret_cast<void*>(round_up(reinterpret_cast<uintptr_t>(workspace), 256));
+  const bool needs_z = act != MF_ACT_NONE;
+  const LinearBwd b{dout, x, Act8{x8, x_scale}, W, needs_z ? z : nullptr,
+                    needs_z ? Act8{z8, z_scale} : Act8{nullptr, nullptr}, tok_mod, act, dx, dW, db};
+  return cuda_status(launch_linear_fused_bwd(b, runs, T, K, N, w0, ctl, stream));
 }
 
 namespace {
