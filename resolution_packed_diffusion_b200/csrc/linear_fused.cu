@@ -25,13 +25,15 @@
 // The sum over a modality's tokens walks its runs of consecutive rows (an image,
 // a text) in steps of 64. The last step of a run may reach into rows of the other
 // modality; there the rows past the run are set to zero in shared memory, in both
-// operands, so that an infinity or NaN in a foreign row has no effect. Warps 8..11
-// do that between the copies and the MMAs, and they turn an 8-bit x into bf16.
+// operands, between the copies and the MMAs, so that an infinity or NaN in a
+// foreign row has no effect. Whole steps go from the copies to the MMAs directly:
+// sending every step through a warp that hands it on across the pair cost 1.0 us a
+// step, against 0.45 us for its copies and MMAs.
 //   warp 0      TMA producer (one lane)
 //   warp 1      tcgen05 issuer (one lane of the leader CTA)
+//   warp 2      dW only: zeroes the rows past a run
 //   warps 4..7  epilogue, one output row per thread, from the accumulator that the
 //               MMAs have left for the other one of the two
-//   warps 8..11 dW only: zero the rows past a run, decode 8-bit x
 // Every wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -55,33 +57,28 @@ constexpr int kTile = 256;   // output tile: rows and columns
 constexpr int kStepK = 64;   // inner dimension per stage: one 128-byte swizzle atom
 constexpr int kBoxBytes = 64 * 64 * 2;  // a 64-column box of 64 rows
 constexpr uint32_t kTmemCols = 512;     // two accumulators of 256 columns
-constexpr int kPrepWarps = 4;
+constexpr int kWarps = 8;
 
-template <int MODE, bool X8>
-struct Layout {
-  static constexpr int A_BYTES = kHalf * kStepK * 2;
-  static constexpr int B_BYTES = kHalf * kStepK * 2;
-  static constexpr int RAW_BYTES = X8 ? kHalf * kStepK : 0;  // int8 codes of x
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + RAW_BYTES;
-  static constexpr int COPY_BYTES = A_BYTES + (X8 ? RAW_BYTES : B_BYTES);  // by TMA, per CTA
-  static constexpr int STAGES = X8 ? 5 : 7;
-  static constexpr int WARPS = MODE == kDw ? 12 : 8;
-  static constexpr int OFF_BAR = STAGES * STAGE_BYTES;
-  // Forward and dx: the leader's FULL counts both CTAs' bytes. dW: each CTA's
-  // copies complete on its own FULL, and READY (the leader's) counts the prep
-  // warps of both. EMPTY and ACC_FULL arrive in both CTAs from the leader's
-  // multicast commits; ACC_EMPTY is the leader's.
-  static constexpr int B_FULL = 0;
-  static constexpr int B_EMPTY = B_FULL + STAGES;
-  static constexpr int B_READY = B_EMPTY + STAGES;
-  static constexpr int B_ACC_FULL = B_READY + (MODE == kDw ? STAGES : 0);
-  static constexpr int B_ACC_EMPTY = B_ACC_FULL + 2;
-  static constexpr int B_DRAIN = B_ACC_EMPTY + 2;
-  static constexpr int NUM_BARS = B_DRAIN + 1;
-  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
-  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
-  static_assert(SMEM_BYTES <= 232448, "shared memory budget of one CTA");
-};
+constexpr int kStages = 7;
+constexpr int kABytes = kHalf * kStepK * 2;
+constexpr int kStageBytes = 2 * kABytes;  // A and B, as copied into one CTA
+
+// Barriers. FULL (the leader's) counts both CTAs' producers and the bytes of both
+// CTAs' copies; for a step that needs rows zeroed the copies complete on their own
+// CTA's PART, and the zeroing warps arrive on FULL in the producers' place. EMPTY
+// and ACC_FULL arrive in both CTAs from the leader's multicast commits; ACC_EMPTY,
+// the leader's, counts both CTAs' epilogue warps.
+constexpr int kFull = 0;
+constexpr int kEmpty = kFull + kStages;
+constexpr int kPart = kEmpty + kStages;
+constexpr int kAccFull = kPart + kStages;
+constexpr int kAccEmpty = kAccFull + 2;
+constexpr int kDrain = kAccEmpty + 2;
+constexpr int kNumBars = kDrain + 1;
+constexpr int kOffBar = kStages * kStageBytes;
+constexpr int kOffMisc = kOffBar + kNumBars * 8;  // TMEM address, abort flag
+constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA");
 
 // One (row block, modality) job per entry for the forward and dx.
 struct RowJobs {
@@ -115,8 +112,6 @@ struct Args {
   int32_t col_tiles;       // column tiles of the output
   int32_t nb;              // column tiles per block of the traversal
   const uint8_t* tok_mod;
-  const float* x_scale;    // dW with 8-bit x: [T][xnb]
-  int32_t xnb;
   LinearEpilogue ep;       // forward: all of it; dx and dW: out
   KernelCtl ctl;
 };
@@ -133,20 +128,11 @@ __device__ __forceinline__ void unit_coords(int u, int rows, int cols, int nb, i
   c = b * nb + (i - r * w);
 }
 
-__device__ __forceinline__ void load_2d(void* dst, const CUtensorMap* map, uint32_t bar, int x,
-                                        int y, bool pair) {
-  if (pair)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-        : "memory");
+// Arrives on a barrier of either CTA of the pair and adds `bytes` to what it
+// expects.
+__device__ __forceinline__ void expect_pair(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
 }
 
 // A box of the weights: modality z of the (K, N, 2) map, completing on the
@@ -177,13 +163,35 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint6
     if (globaltimer_ns() - t0 > limit_ns) return;
 }
 
-// mbar_wait for arrivals from both CTAs that release writes to their shared
-// memory: acquires at cluster scope.
+// mbar_wait for arrivals of both CTAs that release writes to their shared memory:
+// acquires at cluster scope. (A cluster fence after a plain wait does the same and
+// costs the issuing thread about a microsecond a step.)
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
                                                   const KernelCtl& ctl, volatile int* abort_flag) {
-  const bool ok = mbar_wait(bar, parity, ctl, abort_flag);
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
-  return ok;
+  if (try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (try_wait_cluster(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > ctl.wait_limit_ns) {
+      *abort_flag = 1;
+      atomicCAS(ctl.err, 0, static_cast<int>(MF_ERR_TIMEOUT));
+      return false;
+    }
+  }
 }
 
 // What a unit of dW covers: modality, tile, and steps [s0, s1) of its runs.
@@ -340,28 +348,22 @@ __device__ __forceinline__ void forward_row(const Args<kFwd>& a, uint32_t taddr,
   }
 }
 
-template <int MODE, bool X8>
-__global__ void __launch_bounds__(Layout<MODE, X8>::WARPS * 32, 1)
+template <int MODE>
+__global__ void __launch_bounds__(kWarps * 32, 1)
     linear_fused_kernel(const __grid_constant__ CUtensorMap map_a,
                         const __grid_constant__ CUtensorMap map_b,
                         const __grid_constant__ Args<MODE> args) {
-  using L = Layout<MODE, X8>;
-  constexpr int kStages = L::STAGES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::NUM_BARS; ++i) {
-      uint32_t count = 1;
-      if (i == L::B_ACC_EMPTY || i == L::B_ACC_EMPTY + 1) count = 8;  // epilogue warps of the pair
-      if (MODE == kDw && i >= L::B_READY && i < L::B_READY + kStages) count = 2 * kPrepWarps;
-      mbar_init(&bars[i], count);
-    }
+    for (int i = 0; i < kNumBars; ++i)
+      mbar_init(&bars[i], i < kFull + kStages ? 2u : i == kAccEmpty || i == kAccEmpty + 1 ? 8u : 1u);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_map(&map_a);
@@ -399,67 +401,70 @@ __global__ void __launch_bounds__(Layout<MODE, X8>::WARPS * 32, 1)
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t keep = keep_in_l2();
-      uint32_t it = 0;
+      uint32_t it = 0, part_uses = 0;  // bit st: parity of PART[st]'s uses
+      uint32_t part_used = 0;          // bit st: used at all
       bool ok = true;
-      auto stage = [&](uint8_t*& sa, uint32_t& bar) -> bool {
-        const int st = it % kStages;
-        if (!mbar_wait(&bars[L::B_EMPTY + st], ((it / kStages) & 1) ^ 1, args.ctl, abort_flag))
-          return false;
-        sa = smem + st * L::STAGE_BYTES;
-        if constexpr (MODE == kDw) {
-          mbar_expect_tx(&bars[L::B_FULL + st], L::COPY_BYTES);
-          bar = smem_u32(&bars[L::B_FULL + st]);
-        } else {
-          // both CTAs' copies complete on the leader's barrier, which the leader
-          // arms for both (a copy that lands first takes its count below zero)
-          if (rank == 0) mbar_expect_tx(&bars[L::B_FULL + st], 2 * L::COPY_BYTES);
-          bar = cluster_addr(&bars[L::B_FULL + st], 0);
-        }
-        return true;
-      };
       for (int u = unit0; u < units && ok; u += stride) {
-        uint8_t* sa;
-        uint32_t bar;
+        DwUnit w;
+        RunWalk walk;
+        int blk = 0, m = 0, ct = 0, steps;
         if constexpr (MODE == kDw) {
-          const DwUnit w = dw_unit(args, u);
-          RunWalk walk;
+          w = dw_unit(args, u);
           walk.start(args, w.m, w.s0);
-          const int xa = w.nt * kTile + rank * kHalf, xb = w.kt * kTile + rank * kHalf;
-          for (int s = w.s0; s < w.s1; ++s, ++it, walk.next(args, w.m)) {
-            if (!(ok = stage(sa, bar))) break;
-            load_2d(sa, &map_a, bar, xa, walk.row, false);
-            load_2d(sa + kBoxBytes, &map_a, bar, xa + 64, walk.row, false);
-            if constexpr (X8) {
-              load_2d(sa + L::A_BYTES + L::B_BYTES, &map_b, bar, xb, walk.row, false);
-            } else {
-              load_2d(sa + L::A_BYTES, &map_b, bar, xb, walk.row, false);
-              load_2d(sa + L::A_BYTES + kBoxBytes, &map_b, bar, xb + 64, walk.row, false);
-            }
-          }
+          steps = w.s1 - w.s0;
         } else {
-          int blk = 0, m = 0, ct = 0;
           row_job(u, blk, m, ct);
-          const int row = blk * kTile + rank * kHalf, col = ct * kTile + rank * kHalf;
-          for (int s = 0; s < args.n_steps; ++s, ++it) {
-            if (!(ok = stage(sa, bar))) break;
-            load_2d(sa, &map_a, bar, s * kStepK, row, true);
-            if constexpr (MODE == kFwd) {
-              load_w(sa + L::A_BYTES, &map_b, bar, s * kStepK, col, m, keep);
+          steps = args.n_steps;
+        }
+        for (int s = 0; s < steps; ++s, ++it) {
+          const int st = it % kStages;
+          if (!(ok = mbar_wait(&bars[kEmpty + st], ((it / kStages) & 1) ^ 1, args.ctl, abort_flag)))
+            break;
+          uint8_t* sa = smem + st * kStageBytes;
+          uint8_t* sb = sa + kABytes;
+          if constexpr (MODE == kDw) {
+            const int xa = w.nt * kTile + rank * kHalf, xb = w.kt * kTile + rank * kHalf;
+            if (walk.left < kStepK) {
+              mbar_expect_tx(&bars[kPart + st], kStageBytes);
+              tma_load_2d(sa, &map_a, &bars[kPart + st], xa, walk.row);
+              tma_load_2d(sa + kBoxBytes, &map_a, &bars[kPart + st], xa + 64, walk.row);
+              tma_load_2d(sb, &map_b, &bars[kPart + st], xb, walk.row);
+              tma_load_2d(sb + kBoxBytes, &map_b, &bars[kPart + st], xb + 64, walk.row);
+              part_uses ^= 1u << st;
+              part_used |= 1u << st;
             } else {
-              load_w(sa + L::A_BYTES, &map_b, bar, col, s * kStepK, m, keep);
-              load_w(sa + L::A_BYTES + kBoxBytes, &map_b, bar, col + 64, s * kStepK, m, keep);
+              const uint32_t bar = cluster_addr(&bars[kFull + st], 0);
+              expect_pair(bar, kStageBytes);
+              tma_load_2d_pair(sa, &map_a, bar, xa, walk.row);
+              tma_load_2d_pair(sa + kBoxBytes, &map_a, bar, xa + 64, walk.row);
+              tma_load_2d_pair(sb, &map_b, bar, xb, walk.row);
+              tma_load_2d_pair(sb + kBoxBytes, &map_b, bar, xb + 64, walk.row);
+            }
+            walk.next(args, w.m);
+          } else {
+            const int row = blk * kTile + rank * kHalf, col = ct * kTile + rank * kHalf;
+            const uint32_t bar = cluster_addr(&bars[kFull + st], 0);
+            expect_pair(bar, kStageBytes);
+            tma_load_2d_pair(sa, &map_a, bar, s * kStepK, row);
+            if constexpr (MODE == kFwd) {
+              load_w(sb, &map_b, bar, s * kStepK, col, m, keep);
+            } else {
+              load_w(sb, &map_b, bar, col, s * kStepK, m, keep);
+              load_w(sb + kBoxBytes, &map_b, bar, col + 64, s * kStepK, m, keep);
             }
           }
         }
       }
-      // Every copy this thread started, or whose barrier is this CTA's, lands
-      // before the CTA can exit.
-      if (MODE == kDw || rank == 0)
-        for (int st = 0; st < kStages; ++st)
-          if (it > static_cast<uint32_t>(st)) {
-            const uint32_t last = it - 1 - ((it - 1 - st) % kStages);
-            drain_wait(&bars[L::B_FULL + st], (last / kStages) & 1, args.ctl.wait_limit_ns);
-          }
+      // Every copy lands before the CTA whose barrier it completes on can exit: the
+      // leader waits for both CTAs' on FULL, each CTA for its own on PART.
+      for (int st = 0; st < kStages; ++st) {
+        if (rank == 0 && it > static_cast<uint32_t>(st)) {
+          const uint32_t last = it - 1 - ((it - 1 - st) % kStages);
+          drain_wait(&bars[kFull + st], (last / kStages) & 1, args.ctl.wait_limit_ns);
+        }
+        if ((part_used >> st) & 1)
+          drain_wait(&bars[kPart + st], ((part_uses >> st) & 1) ^ 1, args.ctl.wait_limit_ns);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -471,17 +476,19 @@ __global__ void __launch_bounds__(Layout<MODE, X8>::WARPS * 32, 1)
       constexpr uint64_t A_STEP = A_MN ? 128 : 2, B_STEP = B_MN ? 128 : 2;
       const uint32_t base = smem_u32(smem);
       const uint64_t a_desc = sdesc_sw128(base, A_MN ? kBoxBytes : 16, 1024);
-      const uint64_t b_desc = sdesc_sw128(base + L::A_BYTES, B_MN ? kBoxBytes : 16, 1024);
+      const uint64_t b_desc = sdesc_sw128(base + kABytes, B_MN ? kBoxBytes : 16, 1024);
       uint32_t it = 0, ul = 0;
       bool ok = true;
       for (int u = unit0; u < units && ok; u += stride, ++ul) {
         const uint32_t acc = ul & 1;
-        if (!mbar_wait(&bars[L::B_ACC_EMPTY + acc], ((ul >> 1) & 1) ^ 1, args.ctl, abort_flag))
-          break;
+        if (!mbar_wait(&bars[kAccEmpty + acc], ((ul >> 1) & 1) ^ 1, args.ctl, abort_flag)) break;
         tc_fence_after();
-        int steps;
+        int steps, m = 0;
+        RunWalk walk;
         if constexpr (MODE == kDw) {
           const DwUnit w = dw_unit(args, u);
+          m = w.m;
+          walk.start(args, m, w.s0);
           steps = w.s1 - w.s0;
         } else {
           steps = args.n_steps;
@@ -489,35 +496,40 @@ __global__ void __launch_bounds__(Layout<MODE, X8>::WARPS * 32, 1)
         const uint32_t d = tmem + acc * kTile;
         for (int s = 0; s < steps; ++s, ++it) {
           const int st = it % kStages;
-          if constexpr (MODE == kDw)
-            ok = mbar_wait_cluster(&bars[L::B_READY + st], (it / kStages) & 1, args.ctl, abort_flag);
-          else
-            ok = mbar_wait(&bars[L::B_FULL + st], (it / kStages) & 1, args.ctl, abort_flag);
+          const uint32_t parity = (it / kStages) & 1;
+          if constexpr (MODE == kDw) {
+            // zeroed rows were written by threads of both CTAs
+            ok = walk.left < kStepK ? mbar_wait_cluster(&bars[kFull + st], parity, args.ctl, abort_flag)
+                                    : mbar_wait(&bars[kFull + st], parity, args.ctl, abort_flag);
+            walk.next(args, m);
+          } else {
+            ok = mbar_wait(&bars[kFull + st], parity, args.ctl, abort_flag);
+          }
           if (!ok) break;
           tc_fence_after();
-          const uint64_t so = static_cast<uint64_t>((st * L::STAGE_BYTES) >> 4);
+          const uint64_t so = static_cast<uint64_t>((st * kStageBytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < kStepK / 16; ++kk)
             umma_ss_pair(d, a_desc + so + kk * A_STEP, b_desc + so + kk * B_STEP, IDESC,
                          (s > 0 || kk > 0) ? 1u : 0u);
-          umma_commit_pair(&bars[L::B_EMPTY + st], 3);
+          umma_commit_pair(&bars[kEmpty + st], 3);
         }
         if (!ok) break;
-        umma_commit_pair(&bars[L::B_ACC_FULL + acc], 3);
+        umma_commit_pair(&bars[kAccFull + acc], 3);
       }
       // every MMA this thread issued completes before TMEM is released
-      umma_commit_pair(&bars[L::B_DRAIN], 1);
-      drain_wait(&bars[L::B_DRAIN], 0, args.ctl.wait_limit_ns);
+      umma_commit_pair(&bars[kDrain], 1);
+      drain_wait(&bars[kDrain], 0, args.ctl.wait_limit_ns);
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp >= 4) {
     const int wq = warp & 3;
     const int row = wq * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
     uint32_t ul = 0;
     for (int u = unit0; u < units; u += stride, ++ul) {
       const uint32_t acc = ul & 1;
-      if (!warp_wait(&bars[L::B_ACC_FULL + acc], (ul >> 1) & 1, args.ctl, abort_flag)) break;
+      if (!warp_wait(&bars[kAccFull + acc], (ul >> 1) & 1, args.ctl, abort_flag)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + lane_base + acc * kTile;
       if constexpr (MODE == kDw) {
@@ -565,61 +577,32 @@ __global__ void __launch_bounds__(Layout<MODE, X8>::WARPS * 32, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars[L::B_ACC_EMPTY + acc], 0));
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars[kAccEmpty + acc], 0));
     }
-  } else if (MODE == kDw && warp >= 8) {
+  } else if (MODE == kDw && warp == 2) {
     if constexpr (MODE == kDw) {
-      const int tid = threadIdx.x - 8 * 32;
-      uint32_t it = 0;
+      uint32_t it = 0, part_uses = 0;
       bool ok = true;
       for (int u = unit0; u < units && ok; u += stride) {
         const DwUnit w = dw_unit(args, u);
         RunWalk walk;
         walk.start(args, w.m, w.s0);
         for (int s = w.s0; s < w.s1; ++s, ++it, walk.next(args, w.m)) {
+          const int live = walk.left;
+          if (live >= kStepK) continue;
           const int st = it % kStages;
-          const int live = min(walk.left, kStepK);
-          uint8_t* sa = smem + st * L::STAGE_BYTES;
-          float scale = 0.f;
-          if constexpr (X8) {
-            // this thread's row of the step and its 64-column box; a CTA's 128
-            // columns are one block of scales
-            const int kb = (w.kt * kTile + rank * kHalf) / kAct8Block;
-            if ((tid & 63) < live && kb < args.xnb)
-              scale = __ldg(args.x_scale + static_cast<size_t>(walk.row + (tid & 63)) * args.xnb + kb);
-          }
-          if (!(ok = warp_wait(&bars[L::B_FULL + st], (it / kStages) & 1, args.ctl, abort_flag)))
-            break;
-          if constexpr (X8) {
-            // row r of a box is 128 bytes, its 16-byte chunks permuted by r mod 8
-            // (the swizzle); the codes' tile has 128-byte rows swizzled the same way
-            const int r = tid & 63, box = tid >> 6;
-            const uint8_t* codes = sa + L::A_BYTES + L::B_BYTES + r * 128;
-            uint8_t* dst = sa + L::A_BYTES + box * kBoxBytes + r * 128;
+          if (!(ok = warp_wait(&bars[kPart + st], (part_uses >> st) & 1, args.ctl, abort_flag))) break;
+          part_uses ^= 1u << st;
+          // rows past the run in the four 64-column boxes: 128 bytes a row
+          const int dead = (kStepK - live) * 8;
+          uint8_t* sa = smem + st * kStageBytes + live * 128;
+          for (int i = lane; i < dead; i += 32)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint4 q = make_uint4(0, 0, 0, 0);
-              if (r < live) q = *reinterpret_cast<const uint4*>(codes + (((box * 4 + c) ^ (r & 7)) << 4));
-              float f[8];
-              act8_load(make_uint2(q.x, q.y), scale, f);
-              *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (r & 7)) << 4)) = bf16x8_pack(f);
-              act8_load(make_uint2(q.z, q.w), scale, f);
-              *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (r & 7)) << 4)) = bf16x8_pack(f);
-            }
-          }
-          if (live < kStepK) {
-            // rows past the run: A, and B where no decoding has left zeros there
-            const int boxes = X8 ? 2 : 4;
-            for (int i = tid; i < boxes * (kStepK - live) * 8; i += kPrepWarps * 32) {
-              const int b = i / ((kStepK - live) * 8), o = i - b * (kStepK - live) * 8;
-              *reinterpret_cast<uint4*>(sa + b * kBoxBytes + live * 128 + o * 16) =
-                  make_uint4(0, 0, 0, 0);
-            }
-          }
-          // this thread's writes before the tensor core's reads
-          if (X8 || live < kStepK) fence_proxy_async_smem();
+            for (int b = 0; b < 4; ++b)
+              *reinterpret_cast<uint4*>(sa + b * kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();  // this thread's writes before the tensor core's reads
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars[L::B_READY + st], 0));
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars[kFull + st], 0));
         }
       }
     }
@@ -787,31 +770,29 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// [sets][rows][cols] with boxes of box_cols x box_rows, 128-byte swizzle; what
+// [sets][rows][cols] bf16 with boxes of 64 columns x box_rows, 128-byte swizzle; what
 // lies outside reads as zeros. sets 0: a two-dimensional map.
-bool make_map(CUtensorMap* map, const void* base, bool bytes, int64_t cols, int64_t rows, int sets,
-              int box_cols, int box_rows) {
+bool make_map(CUtensorMap* map, const mf_bf16* base, int64_t cols, int64_t rows, int sets,
+              int box_rows) {
   const EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return false;
-  const int64_t esize = bytes ? 1 : 2;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                               static_cast<cuuint64_t>(sets)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols * esize),
-                                 static_cast<cuuint64_t>(cols * rows * esize)};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols * 2),
+                                 static_cast<cuuint64_t>(cols * rows * 2)};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-             sets > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, sets > 0 ? 3 : 2, const_cast<mf_bf16*>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, bool X8>
+template <int MODE>
 cudaLaunchConfig_t config(int clusters, cudaLaunchAttribute* attr, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters);
-  cfg.blockDim = dim3(Layout<MODE, X8>::WARPS * 32);
-  cfg.dynamicSmemBytes = Layout<MODE, X8>::SMEM_BYTES;
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -823,34 +804,34 @@ cudaLaunchConfig_t config(int clusters, cudaLaunchAttribute* attr, cudaStream_t 
 }
 
 // Clusters of two that can be resident at once; 0 if the kernel cannot run.
-template <int MODE, bool X8>
+template <int MODE>
 int max_clusters() {
   static int cached[64] = {0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   if (cached[dev] == 0) {
-    if (cudaFuncSetAttribute(linear_fused_kernel<MODE, X8>,
+    if (cudaFuncSetAttribute(linear_fused_kernel<MODE>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Layout<MODE, X8>::SMEM_BYTES) != cudaSuccess)
+                             kSmemBytes) != cudaSuccess)
       return 0;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = config<MODE, X8>(1, attr, nullptr);
+    cudaLaunchConfig_t cfg = config<MODE>(1, attr, nullptr);
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, linear_fused_kernel<MODE, X8>, &cfg) != cudaSuccess)
+    if (cudaOccupancyMaxActiveClusters(&n, linear_fused_kernel<MODE>, &cfg) != cudaSuccess)
       return 0;
     cached[dev] = n;
   }
   return cached[dev];
 }
 
-template <int MODE, bool X8>
+template <int MODE>
 cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const Args<MODE>& a,
                            int units, cudaStream_t st) {
-  const int mc = max_clusters<MODE, X8>();
+  const int mc = max_clusters<MODE>();
   if (mc <= 0) return cudaErrorInvalidConfiguration;
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = config<MODE, X8>(units < mc ? units : mc, attr, st);
-  return cudaLaunchKernelEx(&cfg, linear_fused_kernel<MODE, X8>, ma, mb, a);
+  cudaLaunchConfig_t cfg = config<MODE>(units < mc ? units : mc, attr, st);
+  return cudaLaunchKernelEx(&cfg, linear_fused_kernel<MODE>, ma, mb, a);
 }
 
 int tiles_of(int64_t v) { return static_cast<int>((v + kTile - 1) / kTile); }
@@ -930,8 +911,8 @@ cudaError_t launch_linear_fused(const mf_bf16* x, const mf_bf16* W, const TokenR
                                 const uint8_t* tok_mod, int32_t T, int32_t K, int32_t N,
                                 const LinearEpilogue& ep, const KernelCtl& ctl, cudaStream_t st) {
   CUtensorMap ma, mb;
-  if (!make_map(&ma, x, false, K, T, 0, kStepK, kHalf) ||
-      !make_map(&mb, W, false, K, N, 2, kStepK, kHalf))
+  if (!make_map(&ma, x, K, T, 0, kHalf) ||
+      !make_map(&mb, W, K, N, 2, kHalf))
     return cudaErrorInvalidValue;
   static thread_local Args<kFwd> a;
   fill(a, T, K, N, N, ctl);
@@ -939,17 +920,17 @@ cudaError_t launch_linear_fused(const mf_bf16* x, const mf_bf16* W, const TokenR
   a.n_steps = (K + kStepK - 1) / kStepK;
   a.tok_mod = tok_mod;
   a.ep = ep;
-  return launch_product<kFwd, false>(ma, mb, a, a.j.jobs.n * a.col_tiles, st);
+  return launch_product<kFwd>(ma, mb, a, a.j.jobs.n * a.col_tiles, st);
 }
 
-// Workspace, in this order: dz [T][N] bf16; db's partials; x in bf16 (an 8-bit x
-// whose rows TMA cannot address); dW's parts.
+// Workspace, in this order: dz [T][N] bf16; db's partials; an 8-bit x in bf16; dW's
+// parts.
 size_t linear_fused_bwd_ws(int32_t T, int32_t K, int32_t N) {
   const size_t chunks = static_cast<size_t>((T + kDzRows - 1) / kDzRows);
   const int tiles = tiles_of(N) * tiles_of(K);
   const size_t parts = tiles * 2 <= kPairs ? static_cast<size_t>(2) * kPairs : 0;
   return round256(static_cast<size_t>(T) * N * 2) + round256(chunks * 2 * N * sizeof(float)) +
-         (K % 16 != 0 ? round256(static_cast<size_t>(T) * K * 2) : 0) +
+         round256(static_cast<size_t>(T) * K * 2) +
          parts * kTile * kTile * sizeof(float);
 }
 
@@ -962,7 +943,7 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
   float* part = reinterpret_cast<float*>(w);
   w += round256(static_cast<size_t>(chunks) * 2 * N * sizeof(float));
   mf_bf16* x_ws = reinterpret_cast<mf_bf16*>(w);
-  if (K % 16 != 0) w += round256(static_cast<size_t>(T) * K * 2);
+  w += round256(static_cast<size_t>(T) * K * 2);
   float* dw_part = reinterpret_cast<float*>(w);
   cudaError_t e;
 
@@ -987,8 +968,8 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
 
   if (b.dx != nullptr) {
     CUtensorMap ma, mb;
-    if (!make_map(&ma, dz, false, N, T, 0, kStepK, kHalf) ||
-        !make_map(&mb, b.W, false, K, N, 2, 64, kStepK))
+    if (!make_map(&ma, dz, N, T, 0, kHalf) ||
+        !make_map(&mb, b.W, K, N, 2, kStepK))
       return cudaErrorInvalidValue;
     static thread_local Args<kDx> a;
     fill(a, T, K, N, K, ctl);
@@ -997,30 +978,28 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
     a.tok_mod = b.tok_mod;
     a.ep = LinearEpilogue{};
     a.ep.out = b.dx;
-    e = launch_product<kDx, false>(ma, mb, a, a.j.jobs.n * a.col_tiles, st);
+    e = launch_product<kDx>(ma, mb, a, a.j.jobs.n * a.col_tiles, st);
     if (e != cudaSuccess) return e;
   }
 
   if (b.dW != nullptr) {
-    // TMA rows of 8-bit codes need a width that is a multiple of 16
-    const bool direct8 = b.x == nullptr && K % 16 == 0;
+    // An 8-bit x is decoded once into the workspace (3 bytes of traffic a value, a
+    // tenth of the product's time at 8464 x 12288 x 3072); decoding it between the
+    // copies and the MMAs, again for every 256 output rows, took 2.6 times as long
+    // as the product.
     const mf_bf16* x = b.x;
-    if (b.x == nullptr && !direct8) {
+    if (x == nullptr) {
       if ((e = launch_act8_dequantize(b.x8.q, b.x8.scale, T, K, MF_ACT_NONE, x_ws, st)) != cudaSuccess)
         return e;
       x = x_ws;
     }
     CUtensorMap ma, mb;
-    if (!make_map(&ma, dz, false, N, T, 0, 64, kStepK) ||
-        !(direct8 ? make_map(&mb, b.x8.q, true, K, T, 0, kHalf, kStepK)
-                  : make_map(&mb, x, false, K, T, 0, 64, kStepK)))
+    if (!make_map(&ma, dz, N, T, 0, kStepK) || !make_map(&mb, x, K, T, 0, kStepK))
       return cudaErrorInvalidValue;
     static thread_local Args<kDw> a;
     fill(a, T, K, N, K, ctl);
     a.ep = LinearEpilogue{};
     a.ep.out = b.dW;
-    a.x_scale = b.x8.scale;
-    a.xnb = act8_blocks(K);
     a.j.part = dw_part;
     const int tiles = tiles_of(N) * a.col_tiles;
     for (int m = 0; m < 2; ++m) {
@@ -1044,8 +1023,7 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
       a.j.units[m] = tiles * a.j.splits[m];
     }
     const int units = a.j.units[0] + a.j.units[1];
-    e = direct8 ? launch_product<kDw, true>(ma, mb, a, units, st)
-                : launch_product<kDw, false>(ma, mb, a, units, st);
+    e = launch_product<kDw>(ma, mb, a, units, st);
     if (e != cudaSuccess) return e;
     float* part = dw_part;
     for (int m = 0; m < 2; ++m) {
