@@ -61,11 +61,14 @@ __global__ void __launch_bounds__(kThreads) act8_quantize_kernel(const mf_bf16* 
     uint32_t m = absmax_bits(v[u]);
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float s, inv, f[8];
+    float s, inv;
+    uint64_t f[4];
     act8_scale(__uint_as_float(m << 16), s, inv);
-    bf16x8_unpack(v[u], f);
+    const uint32_t mask = inv == 0.f ? 0u : 0xFFFFFFFFu;
+    bf16x8_f2(v[u], f);
     if (in[u])
-      __stcs(reinterpret_cast<uint2*>(q + off[u]), make_uint2(act8_code4(f, inv), act8_code4(f + 4, inv)));
+      __stcs(reinterpret_cast<uint2*>(q + off[u]),
+             make_uint2(act8_code4(f[0], f[1], inv, mask), act8_code4(f[2], f[3], inv, mask)));
     const int64_t item = base + u * kPerCta;
     if (lane == 0 && item < items) scale[item] = s;
   }
@@ -94,11 +97,11 @@ __global__ void __launch_bounds__(kThreads) act8_dequantize_kernel(const int8_t*
   }
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    float f[8];
+    uint64_t f[4];
     act8_load(v[u], s[u], f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = act_fwd<ACT>(f[e]);
-    if (in[u]) __stcs(reinterpret_cast<uint4*>(y + off[u]), bf16x8_pack(f));
+    for (int e = 0; e < 4; ++e) f[e] = act_fwd2<ACT>(f[e]);
+    if (in[u]) __stcs(reinterpret_cast<uint4*>(y + off[u]), f2_bf16x8(f));
   }
 }
 

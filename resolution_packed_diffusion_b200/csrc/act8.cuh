@@ -10,6 +10,33 @@
 
 namespace mf {
 
+// Values travel in pairs (f32x2 instructions: one for two values).
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_both(float v) { return f2_pack(v, v); }
+
+__device__ __forceinline__ uint64_t bf16x2_f2(uint32_t w) {
+  return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t f2_bf16x2(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+
+__device__ __forceinline__ void bf16x8_f2(const uint4& u, uint64_t (&f)[4]) {
+  f[0] = bf16x2_f2(u.x);
+  f[1] = bf16x2_f2(u.y);
+  f[2] = bf16x2_f2(u.z);
+  f[3] = bf16x2_f2(u.w);
+}
+__device__ __forceinline__ uint4 f2_bf16x8(const uint64_t (&f)[4]) {
+  return make_uint4(f2_bf16x2(f[0]), f2_bf16x2(f[1]), f2_bf16x2(f[2]), f2_bf16x2(f[3]));
+}
+
 __device__ __forceinline__ void bf16x8_unpack(const uint4& u, float (&f)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -24,22 +51,19 @@ __device__ __forceinline__ uint4 bf16x8_pack(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
-// Four signed bytes as floats: byte b ^ 0x80 in the low mantissa bits of 2^23
-// is 2^23 + b + 128, exactly; one byte permute and one subtraction a value, off
+// Eight codes as values. Byte b ^ 0x80 in the low mantissa bits of 2^23 is
+// 2^23 + b + 128, exactly: one byte permute a value and one subtraction a pair, off
 // the quarter-rate integer conversion path.
-__device__ __forceinline__ void s8x4_float(uint32_t w, float* f) {
-  const uint32_t u = w ^ 0x80808080u;
-  f[0] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440)) - 8388736.f;
-  f[1] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441)) - 8388736.f;
-  f[2] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442)) - 8388736.f;
-  f[3] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443)) - 8388736.f;
-}
-
-__device__ __forceinline__ void act8_load(const uint2& q, float s, float (&f)[8]) {
-  s8x4_float(q.x, f);
-  s8x4_float(q.y, f + 4);
+__device__ __forceinline__ void act8_load(const uint2& q, float s, uint64_t (&f)[4]) {
+  const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
+  const uint64_t bias = f2_both(-8388736.f), s2 = f2_both(s);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] *= s;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = w[i >> 1];
+    const uint32_t lo = __byte_perm(u, 0x4B000000u, (i & 1) ? 0x7442 : 0x7440);
+    const uint32_t hi = __byte_perm(u, 0x4B000000u, (i & 1) ? 0x7443 : 0x7441);
+    f[i] = f2_mul(f2_add(f2_pack(__uint_as_float(lo), __uint_as_float(hi)), bias), s2);
+  }
 }
 
 // Scale and reciprocal step of a block whose largest |x| is `amax` (its bit
@@ -54,48 +78,98 @@ __device__ __forceinline__ void act8_scale(float amax, float& s, float& inv) {
   inv = bad || zero ? 0.f : __fdiv_rn(127.f, amax);
 }
 
-// Code of x under the reciprocal step inv (0 in a zero or non-finite block):
-// round to nearest even of the rounded product, so |code| <= 127. Adding
-// 1.5 * 2^23 leaves the integer in the low bits of the sum.
-__device__ __forceinline__ uint32_t act8_code(float x, float inv) {
-  const float p = inv == 0.f ? 0.f : __fmul_rn(x, inv);
-  return __float_as_uint(__fadd_rn(p, 12582912.f)) & 0xFFu;
+// Four codes of (a.lo, a.hi, b.lo, b.hi) under the reciprocal step: round to nearest
+// even of the rounded product, so |code| <= 127 (1.5 * 2^23 added, the integer is
+// in the low bits of the sum). The products are scalar: the compiler contracts a
+// packed product and sum to one rounding, which moves the ties at x = amax / 2.
+// `mask` is 0 in a zero or non-finite block.
+__device__ __forceinline__ uint32_t act8_code4(uint64_t a, uint64_t b, float inv, uint32_t mask) {
+  const uint64_t round = f2_both(12582912.f);
+  float c0, c1, c2, c3;
+  f2_unpack(a, c0, c1);
+  f2_unpack(b, c2, c3);
+  f2_unpack(f2_add(f2_pack(__fmul_rn(c0, inv), __fmul_rn(c1, inv)), round), c0, c1);
+  f2_unpack(f2_add(f2_pack(__fmul_rn(c2, inv), __fmul_rn(c3, inv)), round), c2, c3);
+  const uint32_t lo = __byte_perm(__float_as_uint(c0), __float_as_uint(c1), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(c2), __float_as_uint(c3), 0x0040);
+  return __byte_perm(lo, hi, 0x5410) & mask;
 }
 
-__device__ __forceinline__ uint32_t act8_code4(const float* x, float inv) {
-  const uint32_t a = act8_code(x[0], inv), b = act8_code(x[1], inv), c = act8_code(x[2], inv),
-                 d = act8_code(x[3], inv);
-  return a | (b << 8) | (c << 16) | (d << 24);
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-// act(z) and act'(z). GELU, tanh form: 0.5 z (1 + tanh u) = z sigma(2u) with
-// u = sqrt(2/pi) (z + 0.044715 z^3); SiLU: z sigma(z). Both are z sigma(w) with
-// w = c1 z + c3 z^3, so act' = sigma + z sigma (1 - sigma) w'. sigma(w) =
-// 1 / (1 + e^-w): e^-w overflows to infinity for large negative w, where the
-// reciprocal is 0 as it should be, and 0 * z stays 0 for finite z.
-struct ActValue {
-  float f, d;
+// act(z) and act'(z) of pairs. GELU, tanh form: 0.5 z (1 + tanh u) = z sigma(2u) with
+// u = sqrt(2/pi) (z + 0.044715 z^3); SiLU: z sigma(z). Both are z sigma(w), w = c1 z +
+// c3 z^3, so act' = sigma + z sigma (1 - sigma) w'. sigma(w) = 1 / (1 + 2^v), v = -w
+// log2(e); a pair shares one reciprocal, 1 / ((1 + a)(1 + b)), since two special
+// functions a value already bound these kernels. z is held at kActLow, where act and
+// act' are below 1e-16 in magnitude, so that the product cannot overflow (2^v < 2^62);
+// act' holds it at 30 too, where sigma is 1. NaN stays NaN.
+template <int ACT>
+struct ActCoef;
+template <>
+struct ActCoef<MF_ACT_GELU> {
+  static constexpr float low = -7.5f;
+  static constexpr float v1 = -2.302208198f, v3 = -0.1029432397f;  // -log2(e) (c1, c3)
+  static constexpr float d1 = 1.5957691216f, d3 = 0.2140644488f;   // w' = c1 + 3 c3 z^2
 };
+template <>
+struct ActCoef<MF_ACT_SILU> {
+  static constexpr float low = -42.f;
+  static constexpr float v1 = -1.442695041f, v3 = 0.f;
+  static constexpr float d1 = 1.f, d3 = 0.f;
+};
+
 template <int ACT>
-__device__ __forceinline__ float act_sigma(float z) {
-  float w = z;
-  if constexpr (ACT == MF_ACT_GELU) w = z * fmaf(0.07135481627f, z * z, 1.5957691216f);
-  return __fdividef(1.f, 1.f + __expf(-w));
+__device__ __forceinline__ uint64_t act_sigma2(uint64_t z, uint64_t zz) {
+  using C = ActCoef<ACT>;
+  const uint64_t v = ACT == MF_ACT_GELU
+                         ? f2_mul(z, f2_fma(zz, f2_both(C::v3), f2_both(C::v1)))
+                         : f2_mul(z, f2_both(C::v1));
+  float a, b;
+  f2_unpack(v, a, b);
+  a = 1.f + ex2_approx(a);
+  b = 1.f + ex2_approx(b);
+  const float r = rcp_approx(a * b);
+  return f2_mul(f2_both(r), f2_pack(b, a));
 }
+
 template <int ACT>
-__device__ __forceinline__ float act_fwd(float z) {
+__device__ __forceinline__ uint64_t act_fwd2(uint64_t z) {
   if constexpr (ACT == MF_ACT_NONE) return z;
-  return z * act_sigma<ACT>(z);
+  else {
+    float a, b;
+    f2_unpack(z, a, b);
+    z = f2_pack(max_nan(a, ActCoef<ACT>::low), max_nan(b, ActCoef<ACT>::low));
+    return f2_mul(z, act_sigma2<ACT>(z, f2_mul(z, z)));
+  }
 }
+
 template <int ACT>
-__device__ __forceinline__ float act_grad(float z) {
-  if constexpr (ACT == MF_ACT_NONE) return 1.f;
-  const float s = act_sigma<ACT>(z);
-  float dw = 1.f;
-  if constexpr (ACT == MF_ACT_GELU) dw = fmaf(0.2140644488f, z * z, 1.5957691216f);
-  // past the saturation of sigma, z w' may overflow while its factor is 0
-  const float t = s * (1.f - s);
-  return t == 0.f ? s : fmaf(z * dw, t, s);
+__device__ __forceinline__ uint64_t act_grad2(uint64_t z) {
+  using C = ActCoef<ACT>;
+  float a, b;
+  f2_unpack(z, a, b);
+  z = f2_pack(min_nan(max_nan(a, C::low), 30.f), min_nan(max_nan(b, C::low), 30.f));
+  const uint64_t zz = f2_mul(z, z);
+  const uint64_t s = act_sigma2<ACT>(z, zz);
+  uint64_t zd = z;  // z w'
+  if constexpr (ACT == MF_ACT_GELU) zd = f2_mul(z, f2_fma(zz, f2_both(C::d3), f2_both(C::d1)));
+  // s + z w' (s - s^2)
+  return f2_fma(zd, f2_fma(f2_mul(s, f2_both(-1.f)), s, s), s);
 }
 
 }  // namespace mf

@@ -8,17 +8,24 @@
 //
 // Both passes are bound by HBM: the forward reads and writes a row once, the
 // backward reads x (bf16, or an 8-bit checkpoint of it), dy and resid once and
-// writes dx. So that nothing else is read per row, a thread owns eight channels
-// for the whole launch: their gamma, beta and, in the backward, their running
-// dgamma and dbeta stay in registers, and a row is shared by a group of threads
-// (8, 16 or 32 lanes, or several warps). A group takes R rows per step and has
-// the next step's loads in flight while it reduces; the row sums are reduced by
-// shuffles and, over several warps, through shared memory at one named barrier.
-// The forward takes the variance about the mean in a second reduction over the
-// rows in registers (no cancellation). The backward's column sums go, whenever
-// the modality of a group's rows changes and at the end, to the group's own place
-// in shared memory, then per CTA to the workspace, then through a second kernel
-// that adds the CTAs in a fixed order: no atomics, the same bits every time.
+// writes dx.
+//
+// Forward, rows of 264 to 4096 channels (layer_norm_rows_kernel): a warp per row,
+// the row in registers for the mean, the variance about the mean (no cancellation)
+// and the output; one persistent CTA per SM, so that gamma and beta of both
+// modalities are read from shared memory and not once more per row from L1 or L2.
+// Narrower and wider rows (layer_norm_kernel): a row is shared by a group of threads
+// (8, 16 or 32 lanes, or several warps), a thread owning eight channels whose gamma
+// and beta stay in registers; R rows per step, the next step's loads in flight.
+//
+// Backward: column ownership as there, since a thread then also keeps its channels'
+// running dgamma and dbeta in registers. A step's rows lie next to each other, so
+// one bulk copy per tensor brings them into a ring of shared-memory stages; the row
+// sums of g and g xhat are reduced by shuffles and, over several warps, at the one
+// barrier a step has, after which dx is formed from the same stage. The column sums
+// leave the registers when the modality changes and at the end, to the group's own
+// place, and a second kernel adds the CTAs' in a fixed order: no atomics, the same
+// bits every time.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -101,6 +108,12 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
   const float4 b = __ldg(reinterpret_cast<const float4*>(p + 4));
   f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+__device__ __forceinline__ void load8_f2(const float* p, uint64_t (&f)[4]) {
+  const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(p));
+  const ulonglong2 b = __ldg(reinterpret_cast<const ulonglong2*>(p) + 1);
+  f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
 }
 
 struct LnArgs {
@@ -211,156 +224,352 @@ __global__ void __launch_bounds__(THREADS) layer_norm_kernel(const mf_bf16* __re
   }
 }
 
-// part: [grid][2 modalities][2 (dgamma, dbeta)][hid], or dgamma / dbeta
-// themselves when the grid is one CTA (part NULL). Shared memory:
-// [groups][2][2][hid] fp32.
-template <int SUB, int R, int THREADS, bool X8>
-__global__ void __launch_bounds__(THREADS) layer_norm_bwd_kernel(
+// One warp per row of NCH x 256 channels at most. Dynamic shared memory:
+// [2 modalities][gamma, beta][2][hid / 8] float4, the first and the second four of
+// every eight channels apart, so that a warp's reads meet no bank twice.
+__device__ __forceinline__ float warp_total(uint64_t pair) {
+  float lo, hi;
+  f2_unpack(pair, lo, hi);
+  lo += hi;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) lo += __shfl_xor_sync(0xffffffffu, lo, o);
+  return lo;
+}
+
+// Warps of a CTA: as many as the registers of a row (and of its passes) leave room for.
+constexpr int row_warps(int nch) { return nch <= 4 ? 24 : nch <= 8 ? 20 : nch <= 12 ? 16 : 12; }
+
+template <int NCH>
+__global__ void __launch_bounds__(row_warps(NCH) * 32, 1)
+    layer_norm_rows_kernel(const mf_bf16* __restrict__ x, const float* __restrict__ gamma,
+                           const float* __restrict__ beta, const LnArgs a, float eps,
+                           mf_bf16* __restrict__ y, float2* __restrict__ stats) {
+  extern __shared__ float4 par[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nc = a.hid >> 3;
+  const float inv_n = 1.f / static_cast<float>(a.hid);
+  constexpr int kRowWarps = row_warps(NCH);
+  const int row0 = blockIdx.x * kRowWarps + warp, stride = gridDim.x * kRowWarps;
+  uint4 v[NCH];
+  for (int i = threadIdx.x; i < 8 * nc; i += blockDim.x) {
+    // i: ((modality * 2 + which) * 2 + half) * nc + chunk
+    const int chunk = i % nc, r = i / nc;
+    const float* src = (r & 2) ? beta : gamma;
+    par[i] = __ldg(reinterpret_cast<const float4*>(src + static_cast<size_t>(r >> 2) * a.hid) +
+                   2 * chunk + (r & 1));
+  }
+  __syncthreads();
+  for (int row = row0; row < a.T; row += stride) {
+    const uint4* xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(row) * a.hid);
+#pragma unroll
+    for (int u = 0; u < NCH; ++u) {
+      const int i = lane + 32 * u;
+      v[u] = i < nc ? __ldcs(xr + i) : make_uint4(0, 0, 0, 0);
+    }
+    const int m = __ldg(a.tok_mod + row);
+    uint64_t acc = 0;
+#pragma unroll
+    for (int u = 0; u < NCH; ++u) {
+      uint64_t f[4];
+      bf16x8_f2(v[u], f);
+      acc = f2_add(acc, f2_add(f2_add(f[0], f[1]), f2_add(f[2], f[3])));
+    }
+    const float mean = warp_total(acc) * inv_n;
+    const uint64_t shift = f2_both(-mean);
+    acc = 0;
+#pragma unroll
+    for (int u = 0; u < NCH; ++u) {
+      if (lane + 32 * u < nc) {
+        uint64_t f[4];
+        bf16x8_f2(v[u], f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t d = f2_add(f[e], shift);
+          acc = f2_fma(d, d, acc);
+        }
+      }
+    }
+    const float rstd = rsqrtf(fmaf(warp_total(acc), inv_n, eps));
+    if (m > 1) {
+      if (lane == 0) atomicCAS(a.ctl.err, 0, static_cast<int>(MF_ERR_INVALID));
+      continue;
+    }
+    const uint64_t scale = f2_both(rstd);
+    const ulonglong2* p = reinterpret_cast<const ulonglong2*>(par + m * 4 * nc);
+    uint4* yr = reinterpret_cast<uint4*>(y + static_cast<size_t>(row) * a.hid);
+#pragma unroll
+    for (int u = 0; u < NCH; ++u) {
+      const int i = lane + 32 * u;
+      if (i < nc) {
+        uint64_t f[4];
+        bf16x8_f2(v[u], f);
+        const ulonglong2 g0 = p[i], g1 = p[nc + i], b0 = p[2 * nc + i], b1 = p[3 * nc + i];
+        f[0] = f2_fma(f2_mul(f2_add(f[0], shift), scale), g0.x, b0.x);
+        f[1] = f2_fma(f2_mul(f2_add(f[1], shift), scale), g0.y, b0.y);
+        f[2] = f2_fma(f2_mul(f2_add(f[2], shift), scale), g1.x, b1.x);
+        f[3] = f2_fma(f2_mul(f2_add(f[3], shift), scale), g1.y, b1.y);
+        __stcs(yr + i, f2_bf16x8(f));
+      }
+    }
+    if (lane == 0 && stats != nullptr) stats[row] = make_float2(mean, rstd);
+  }
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Bytes of one stage's parts (x, dy, resid), each a multiple of 128.
+struct BwdStage {
+  int x, d, r, stages;
+  __host__ __device__ int bytes() const { return x + d + r; }
+};
+
+constexpr int kBwdRows = 2;  // rows per group and step: an even number, so that a
+                             // step's 8-bit codes start on a 16-byte boundary
+constexpr int kMaxStages = 4;
+
+// part: [grid][2 modalities][2 (dgamma, dbeta)][hid], or dgamma and dbeta themselves
+// when the grid is one CTA (part NULL). Dynamic shared memory: the stages, then, with
+// more than one group, [groups][2][2][hid] fp32. One group adds into its place in
+// memory directly: each column has one owner.
+template <int SUB, int THREADS, int PER_SM, bool X8>
+__global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
     const mf_bf16* __restrict__ dy, const mf_bf16* __restrict__ x, const Act8 x8,
     const float* __restrict__ gamma, const float2* __restrict__ stats, const mf_bf16* resid,
-    const LnArgs a, mf_bf16* dx, float* __restrict__ part, float* __restrict__ dgamma,
-    float* __restrict__ dbeta) {
-  extern __shared__ float cols[];
-  __shared__ float red[2 * 32 * 8];
+    const LnArgs a, const BwdStage sg, mf_bf16* dx, float* __restrict__ part,
+    float* __restrict__ dgamma, float* __restrict__ dbeta) {
+  constexpr int R = kBwdRows;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float red[2][32][2 * R];
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
   const int group = threadIdx.x / a.lanes, gl = threadIdx.x - group * a.lanes;
-  const int warps = a.lanes / 32, wig = gl / 32;
+  const int warps = a.lanes / 32;
   const int c = gl * 8;
   const bool on = c < a.hid;
   const float inv_n = 1.f / static_cast<float>(a.hid);
   const int nb = (a.hid + kAct8Block - 1) / kAct8Block;
-  int r0, r1, flip = 0;
+  int r0, r1;
   cta_rows<R>(a, r0, r1);
-  float* mine = cols + static_cast<size_t>(group) * 4 * a.hid;  // [2][2][hid]
-  if (on) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) mine[j * a.hid + c + e] = 0.f;
+  const int step = a.groups * R;
+  const int steps = (r1 - r0 + step - 1) / step;
+  float* cols = reinterpret_cast<float*>(smem + sg.stages * sg.bytes());
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < sg.stages; ++i) mbar_init(&full[i], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
   }
-  float gam[8], ag[8], ab[8];
+  __syncthreads();
+  // thread 0: the rows of step s into its stage
+  auto issue = [&](int s) {
+    const int row = r0 + s * step, rows = min(step, r1 - row);
+    uint8_t* dst = smem + (s % sg.stages) * sg.bytes();
+    uint64_t* bar = &full[s % sg.stages];
+    const size_t off = static_cast<size_t>(row) * a.hid;
+    const uint32_t n = static_cast<uint32_t>(rows) * a.hid;
+    uint32_t nx = 2 * n;
+    if constexpr (X8) {
+      nx = n & ~15u;
+      if (n & 8u)  // an odd last row of an odd width: its last eight codes
+        *reinterpret_cast<uint2*>(dst + nx) = *reinterpret_cast<const uint2*>(x8.q + off + nx);
+    }
+    mbar_expect_tx(bar, nx + 2 * n + (resid != nullptr ? 2 * n : 0));
+    if (nx > 0) {
+      if constexpr (X8)
+        bulk_load(dst, x8.q + off, nx, bar);
+      else
+        bulk_load(dst, x + off, nx, bar);
+    }
+    bulk_load(dst + sg.x, dy + off, 2 * n, bar);
+    if (resid != nullptr) bulk_load(dst + sg.x + sg.d, resid + off, 2 * n, bar);
+  };
+  if (threadIdx.x == 0)
+    for (int s = 0; s < sg.stages && s < steps; ++s) issue(s);
+
+  uint64_t gam[4], ag[4], ab[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) gam[e] = ag[e] = ab[e] = 0.f;
-  int cm = -1;
-  auto flush = [&]() {
-    if (on && cm >= 0) {
-      float* p = mine + cm * 2 * a.hid + c;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        p[e] += ag[e];
-        p[a.hid + e] += ab[e];
-        ag[e] = ab[e] = 0.f;
-      }
+  for (int e = 0; e < 4; ++e) gam[e] = ag[e] = ab[e] = 0;
+  int cm = -1, seen = 0;
+  // this group's place for modality m: dgamma's row, dbeta's row
+  auto place = [&](int m, float*& g, float*& b) {
+    if (a.groups > 1) {
+      g = cols + (static_cast<size_t>(group) * 4 + m * 2) * a.hid + c;
+      b = g + a.hid;
+    } else if (part != nullptr) {
+      g = part + (static_cast<size_t>(blockIdx.x) * 4 + m * 2) * a.hid + c;
+      b = g + a.hid;
+    } else {
+      g = dgamma + static_cast<size_t>(m) * a.hid + c;
+      b = dbeta + static_cast<size_t>(m) * a.hid + c;
     }
   };
-  uint4 nx[R], nd[R];
+  auto flush = [&]() {
+    if (on && cm >= 0) {
+      float *g, *b;
+      place(cm, g, b);
+      const bool more = (seen >> cm) & 1;
+      uint64_t* g2 = reinterpret_cast<uint64_t*>(g);
+      uint64_t* b2 = reinterpret_cast<uint64_t*>(b);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        g2[e] = more ? f2_add(g2[e], ag[e]) : ag[e];
+        b2[e] = more ? f2_add(b2[e], ab[e]) : ab[e];
+        ag[e] = ab[e] = 0;
+      }
+      seen |= 1 << cm;
+    }
+  };
+  // small per-row values of a step, fetched one step ahead
   float2 nst[R];
-  float ns[R];
-  int mod_next[R];
+  float nsc[R];
+  int nmod[R];
   auto fetch = [&](int row) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const bool live = row + i < r1;
-      mod_next[i] = live ? __ldg(a.tok_mod + row + i) : -1;
+      nmod[i] = live ? __ldg(a.tok_mod + row + i) : -1;
       nst[i] = live ? __ldg(stats + row + i) : make_float2(0.f, 0.f);
-      const size_t off = static_cast<size_t>(row + i) * a.hid + c;
-      nx[i] = nd[i] = make_uint4(0, 0, 0, 0);
-      ns[i] = 0.f;
-      if (live && on) {
-        nd[i] = __ldcs(reinterpret_cast<const uint4*>(dy + off));
-        if constexpr (X8) {
-          const uint2 w = __ldcs(reinterpret_cast<const uint2*>(x8.q + off));
-          nx[i].x = w.x;
-          nx[i].y = w.y;
-          ns[i] = __ldg(x8.scale + static_cast<size_t>(row + i) * nb + c / kAct8Block);
-        } else {
-          nx[i] = __ldcs(reinterpret_cast<const uint4*>(x + off));
-        }
-      }
+      nsc[i] = 0.f;
+      if constexpr (X8)
+        if (live && on)
+          nsc[i] = __ldg(x8.scale + static_cast<size_t>(row + i) * nb + c / kAct8Block);
     }
   };
-  const int step = a.groups * R;
   fetch(r0 + group * R);
-  // every group of the CTA takes the same number of steps: its rows past the end
-  // are not live, but its lanes shuffle with their warp's other groups
-  for (int base = r0; base < r1; base += step) {
-    const int row = base + group * R;
-    uint4 vx[R], vd[R], vr[R];
-    float2 st[R];
+  for (int s = 0; s < steps; ++s) {
+    const int row = r0 + s * step + group * R;
+    float2 st[R];  // (mean * rstd, rstd)
     float sc[R];
     int mod[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      vx[i] = nx[i];
-      vd[i] = nd[i];
-      st[i] = nst[i];
-      sc[i] = ns[i];
-      mod[i] = mod_next[i];
-      vr[i] = make_uint4(0, 0, 0, 0);
-      if (resid != nullptr && on && row + i < r1)
-        vr[i] = *reinterpret_cast<const uint4*>(resid + static_cast<size_t>(row + i) * a.hid + c);
+      st[i] = make_float2(nst[i].x * nst[i].y, nst[i].y);
+      sc[i] = nsc[i];
+      mod[i] = nmod[i];
+      if (mod[i] > 1) {
+        if (gl == 0) atomicCAS(a.ctl.err, 0, static_cast<int>(MF_ERR_INVALID));
+        mod[i] = -1;
+      }
     }
     fetch(row + step);
-    auto xhat = [&](int i, float (&h)[8]) {
+    const uint8_t* sx = smem + (s % sg.stages) * sg.bytes();
+    const uint8_t* sd = sx + sg.x;
+    const uint8_t* sr = sd + sg.d;
+    // A wait that runs out is recorded and the step goes on, so that every thread
+    // still meets every barrier.
+    (void)mbar_wait(&full[s % sg.stages], (s / sg.stages) & 1, a.ctl, abort_flag);
+    auto operands = [&](int i, uint64_t (&h)[4], uint64_t (&d)[4]) {
+      const uint32_t at = static_cast<uint32_t>(group * R + i) * a.hid + c;
       if constexpr (X8)
-        act8_load(make_uint2(vx[i].x, vx[i].y), sc[i], h);
+        act8_load(*reinterpret_cast<const uint2*>(sx + at), sc[i], h);
       else
-        bf16x8_unpack(vx[i], h);
+        bf16x8_f2(*reinterpret_cast<const uint4*>(sx + 2 * at), h);
+      bf16x8_f2(*reinterpret_cast<const uint4*>(sd + 2 * at), d);
+      const uint64_t r2 = f2_both(st[i].y), m2 = f2_both(-st[i].x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = (h[e] - st[i].x) * st[i].y;
+      for (int e = 0; e < 4; ++e) h[e] = f2_fma(h[e], r2, m2);
     };
-    // the modality's weights, then the row sums of g and g xhat
     float sums[2 * R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       sums[2 * i] = sums[2 * i + 1] = 0.f;
-      if (mod[i] < 0 || mod[i] > 1) {
-        if (mod[i] > 1 && gl == 0) atomicCAS(a.ctl.err, 0, static_cast<int>(MF_ERR_INVALID));
-        continue;
-      }
+      if (mod[i] < 0) continue;
       if (mod[i] != cm) {
         flush();
         cm = mod[i];
-        if (on) load8(gamma + static_cast<size_t>(cm) * a.hid + c, gam);
+        if (on) load8_f2(gamma + static_cast<size_t>(cm) * a.hid + c, gam);
       }
-      float h[8], d[8];
-      xhat(i, h);
-      bf16x8_unpack(vd[i], d);
       if (on) {
+        uint64_t h[4], d[4], s1 = 0, s2 = 0;
+        operands(i, h, d);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ag[e] = fmaf(d[e], h[e], ag[e]);
-          ab[e] += d[e];
-          const float g = d[e] * gam[e];
-          sums[2 * i] += g;
-          sums[2 * i + 1] = fmaf(g, h[e], sums[2 * i + 1]);
+        for (int e = 0; e < 4; ++e) {
+          ag[e] = f2_fma(d[e], h[e], ag[e]);
+          ab[e] = f2_add(ab[e], d[e]);
+          const uint64_t g = f2_mul(d[e], gam[e]);
+          s1 = f2_add(s1, g);
+          s2 = f2_fma(g, h[e], s2);
         }
+        float lo, hi;
+        f2_unpack(s1, lo, hi);
+        sums[2 * i] = lo + hi;
+        f2_unpack(s2, lo, hi);
+        sums[2 * i + 1] = lo + hi;
       }
     }
-    group_sum<2 * R, SUB>(sums, warps, group, wig, red, flip);
-    float gm[8];
+    // The four sums over a group's lanes. Lane l ends with sum l mod 4: two rounds
+    // that halve the sums a lane holds, then plain ones (6 shuffles in place of 20).
+    const int lane = threadIdx.x & 31;
+    float part4;
+    {
+      const bool odd = lane & 1, upper = lane & 2;
+      float k0 = odd ? sums[1] : sums[0], g0 = odd ? sums[0] : sums[1];
+      float k1 = odd ? sums[3] : sums[2], g1 = odd ? sums[2] : sums[3];
+      k0 += __shfl_xor_sync(0xffffffffu, g0, 1);
+      k1 += __shfl_xor_sync(0xffffffffu, g1, 1);
+      part4 = upper ? k1 : k0;
+      part4 += __shfl_xor_sync(0xffffffffu, upper ? k0 : k1, 2);
+    }
+#pragma unroll
+    for (int o = 4; o < SUB; o <<= 1) part4 += __shfl_xor_sync(0xffffffffu, part4, o);
+    if (SUB == 32 && warps > 1 && lane < 4) red[s & 1][threadIdx.x >> 5][lane] = part4;
+    __syncthreads();
+    // every thread has left the previous step, so its stage can be filled again
+    if (threadIdx.x == 0 && s > 0 && s - 1 + sg.stages < steps) issue(s - 1 + sg.stages);
+    if (SUB == 32 && warps > 1) {
+      // sum l mod 4 of the group's warps, eight of them at a time
+      part4 = 0.f;
+      for (int w = lane >> 2; w < warps; w += 8) part4 += red[s & 1][group * warps + w][lane & 3];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) part4 += __shfl_xor_sync(0xffffffffu, part4, o);
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * R; ++i)
+      sums[i] = __shfl_sync(0xffffffffu, part4, (lane & ~3) | i) * inv_n;
+    if (!on) continue;
+    uint64_t gm[4];
     int gmod = cm;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) gm[e] = gam[e];
+    for (int e = 0; e < 4; ++e) gm[e] = gam[e];
 #pragma unroll
     for (int i = R - 1; i >= 0; --i) {
-      if (mod[i] < 0 || mod[i] > 1) continue;
+      if (mod[i] < 0) continue;
       if (mod[i] != gmod) {  // an earlier row of the step, before the change
         gmod = mod[i];
-        if (on) load8(gamma + static_cast<size_t>(gmod) * a.hid + c, gm);
+        load8_f2(gamma + static_cast<size_t>(gmod) * a.hid + c, gm);
       }
-      if (!on) continue;
-      float h[8], d[8], o[8];
-      xhat(i, h);
-      bf16x8_unpack(vd[i], d);
-      bf16x8_unpack(vr[i], o);
-      const float m1 = sums[2 * i] * inv_n, m2 = sums[2 * i + 1] * inv_n;
+      uint64_t h[4], d[4], o[4] = {0, 0, 0, 0};
+      operands(i, h, d);
+      if (resid != nullptr)
+        bf16x8_f2(*reinterpret_cast<const uint4*>(
+                      sr + 2 * (static_cast<uint32_t>(group * R + i) * a.hid + c)), o);
+      const uint64_t m1 = f2_both(-sums[2 * i]), m2 = f2_both(-sums[2 * i + 1]);
+      const uint64_t r2 = f2_both(st[i].y);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        o[e] = fmaf(d[e] * gm[e] - m1 - h[e] * m2, st[i].y, o[e]);
-      *reinterpret_cast<uint4*>(dx + static_cast<size_t>(row + i) * a.hid + c) = bf16x8_pack(o);
+      for (int e = 0; e < 4; ++e)
+        o[e] = f2_fma(f2_fma(h[e], m2, f2_fma(d[e], gm[e], m1)), r2, o[e]);
+      *reinterpret_cast<uint4*>(dx + static_cast<size_t>(row + i) * a.hid + c) = f2_bf16x8(o);
     }
   }
   flush();
+  if (on) {  // a modality that this group did not meet
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      if ((seen >> m) & 1) continue;
+      float *g, *b;
+      place(m, g, b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[e] = b[e] = 0.f;
+    }
+  }
+  if (a.groups == 1) return;
   __syncthreads();
   // the CTA's groups in order
   for (int i = threadIdx.x; i < 4 * a.hid; i += blockDim.x) {
@@ -407,25 +616,57 @@ cudaError_t fwd_shape(const mf_bf16* x, const float* gamma, const float* beta, c
   return cudaGetLastError();
 }
 
-int bwd_cap(int threads) { return ln_sms() * (threads > 256 ? 1 : 2); }
-
-template <int SUB, int R, int THREADS, bool X8>
-cudaError_t bwd_shape(const mf_bf16* dy, const mf_bf16* x, const Act8& x8, const float* gamma,
-                      const float* stats, const mf_bf16* resid, const LnArgs& a, int threads,
-                      mf_bf16* dx, float* dgamma, float* dbeta, float* part, cudaStream_t st) {
-  auto kernel = layer_norm_bwd_kernel<SUB, R, THREADS, X8>;
-  const size_t smem = static_cast<size_t>(a.groups) * 4 * a.hid * sizeof(float);
-  if (smem > 40960) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+template <int NCH>
+cudaError_t fwd_rows(const mf_bf16* x, const float* gamma, const float* beta, const LnArgs& a,
+                     float eps, mf_bf16* y, float* stats, cudaStream_t st) {
+  auto kernel = layer_norm_rows_kernel<NCH>;
+  const int smem = a.hid * 16;
+  if (smem > 49152) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  const int steps = (a.T + a.groups * R - 1) / (a.groups * R);
-  const int cap = bwd_cap(threads);
+  constexpr int kRowWarps = row_warps(NCH);
+  const int need = (a.T + kRowWarps - 1) / kRowWarps, cap = ln_sms();
+  kernel<<<need < cap ? need : cap, kRowWarps * 32, smem, st>>>(x, gamma, beta, a, eps, y,
+                                                                reinterpret_cast<float2*>(stats));
+  return cudaGetLastError();
+}
+
+// CTAs per SM of the backward: two of up to 512 threads, so that one computes while
+// the other waits at its barrier.
+int bwd_per_sm(int threads) { return threads > 512 ? 1 : 2; }
+
+BwdStage bwd_stage(const RowShape& s, int32_t hid, bool x8, bool resid) {
+  auto round128 = [](int v) { return (v + 127) / 128 * 128; };
+  const int n = s.groups * kBwdRows * hid;
+  BwdStage g;
+  g.x = round128(x8 ? n : 2 * n);
+  g.d = round128(2 * n);
+  g.r = resid ? g.d : 0;
+  const int cols = s.groups > 1 ? s.groups * 16 * hid : 0;
+  const int room = (bwd_per_sm(s.threads) == 2 ? 110 : 220) * 1024 - cols;
+  g.stages = room / g.bytes();
+  if (g.stages > kMaxStages) g.stages = kMaxStages;
+  return g;
+}
+
+template <int SUB, int THREADS, int PER_SM, bool X8>
+cudaError_t bwd_shape(const mf_bf16* dy, const mf_bf16* x, const Act8& x8, const float* gamma,
+                      const float* stats, const mf_bf16* resid, const LnArgs& a, const RowShape& s,
+                      mf_bf16* dx, float* dgamma, float* dbeta, float* part, cudaStream_t st) {
+  auto kernel = layer_norm_bwd_kernel<SUB, THREADS, PER_SM, X8>;
+  const BwdStage g = bwd_stage(s, a.hid, X8, resid != nullptr);
+  const int smem = g.stages * g.bytes() + (s.groups > 1 ? s.groups * 16 * a.hid : 0);
+  const cudaError_t ae =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (ae != cudaSuccess) return ae;
+  const int steps = (a.T + a.groups * kBwdRows - 1) / (a.groups * kBwdRows);
+  const int cap = ln_sms() * bwd_per_sm(s.threads);
   const int grid = steps < cap ? steps : cap;
   float* p = grid > 1 ? part : nullptr;
-  kernel<<<grid, threads, smem, st>>>(dy, x, x8, gamma, reinterpret_cast<const float2*>(stats),
-                                      resid, a, dx, p, dgamma, dbeta);
+  kernel<<<grid, s.threads, smem, st>>>(dy, x, x8, gamma, reinterpret_cast<const float2*>(stats),
+                                        resid, a, g, dx, p, dgamma, dbeta);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p == nullptr) return e;
   ln_cols_kernel<<<(4 * a.hid + 31) / 32, 256, 0, st>>>(p, grid, a.hid, dgamma, dbeta);
@@ -441,14 +682,18 @@ cudaError_t launch_layer_norm(const mf_bf16* x, const float* gamma, const float*
   const LnArgs a{tok_mod, T, hid, s.lanes, s.groups, ctl};
   if (s.lanes == 8) return fwd_shape<8, 4, 256>(x, gamma, beta, a, s.threads, eps, y, stats, st);
   if (s.lanes == 16) return fwd_shape<16, 4, 256>(x, gamma, beta, a, s.threads, eps, y, stats, st);
-  if (s.threads <= 512)
-    return fwd_shape<32, 4, 512>(x, gamma, beta, a, s.threads, eps, y, stats, st);
+  if (s.lanes == 32) return fwd_shape<32, 4, 256>(x, gamma, beta, a, s.threads, eps, y, stats, st);
+  if (hid <= 512) return fwd_rows<2>(x, gamma, beta, a, eps, y, stats, st);
+  if (hid <= 1024) return fwd_rows<4>(x, gamma, beta, a, eps, y, stats, st);
+  if (hid <= 2048) return fwd_rows<8>(x, gamma, beta, a, eps, y, stats, st);
+  if (hid <= 3072) return fwd_rows<12>(x, gamma, beta, a, eps, y, stats, st);
+  if (hid <= 4096) return fwd_rows<16>(x, gamma, beta, a, eps, y, stats, st);
   return fwd_shape<32, 2, 1024>(x, gamma, beta, a, s.threads, eps, y, stats, st);
 }
 
 size_t layer_norm_bwd_ws(int32_t T, int32_t hid) {
   (void)T;
-  return static_cast<size_t>(bwd_cap(row_shape(hid).threads)) * 4 * hid * sizeof(float);
+  return static_cast<size_t>(ln_sms()) * bwd_per_sm(row_shape(hid).threads) * 4 * hid * sizeof(float);
 }
 
 cudaError_t launch_layer_norm_bwd(const mf_bf16* dy, const mf_bf16* x, const Act8& x8,
@@ -459,15 +704,17 @@ cudaError_t launch_layer_norm_bwd(const mf_bf16* dy, const mf_bf16* x, const Act
   const RowShape s = row_shape(hid);
   const LnArgs a{tok_mod, T, hid, s.lanes, s.groups, ctl};
   float* part = reinterpret_cast<float*>(ws);
-#define MF_LN_BWD(SUB, R, THREADS)                                                               \
-  (x8.q != nullptr ? bwd_shape<SUB, R, THREADS, true>(dy, x, x8, gamma, stats, resid, a,         \
-                                                      s.threads, dx, dgamma, dbeta, part, st)    \
-                   : bwd_shape<SUB, R, THREADS, false>(dy, x, x8, gamma, stats, resid, a,        \
-                                                       s.threads, dx, dgamma, dbeta, part, st))
-  if (s.lanes == 8) return MF_LN_BWD(8, 2, 256);
-  if (s.lanes == 16) return MF_LN_BWD(16, 2, 256);
-  if (s.threads <= 512) return MF_LN_BWD(32, 2, 512);
-  return MF_LN_BWD(32, 1, 1024);
+#define MF_LN_BWD(SUB, THREADS, PER_SM)                                                        \
+  (x8.q != nullptr                                                                             \
+       ? bwd_shape<SUB, THREADS, PER_SM, true>(dy, x, x8, gamma, stats, resid, a, s, dx, dgamma, \
+                                               dbeta, part, st)                                \
+       : bwd_shape<SUB, THREADS, PER_SM, false>(dy, x, x8, gamma, stats, resid, a, s, dx, dgamma, \
+                                                dbeta, part, st))
+  if (s.lanes == 8) return MF_LN_BWD(8, 256, 2);
+  if (s.lanes == 16) return MF_LN_BWD(16, 256, 2);
+  if (s.threads <= 384) return MF_LN_BWD(32, 384, 2);
+  if (s.threads <= 512) return MF_LN_BWD(32, 512, 2);
+  return MF_LN_BWD(32, 1024, 1);
 #undef MF_LN_BWD
 }
 

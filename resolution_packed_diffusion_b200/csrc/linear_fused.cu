@@ -32,8 +32,8 @@
 //   warp 0      TMA producer (one lane)
 //   warp 1      tcgen05 issuer (one lane of the leader CTA)
 //   warp 2      dW only: zeroes the rows past a run
-//   warps 4..7  epilogue, one output row per thread, from the accumulator that the
-//               MMAs have left for the other one of the two
+//   warps 4..11 epilogue, from the accumulator that the MMAs have left for the other
+//               one of the two: one output row and half of the columns per thread
 // Every wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -53,11 +53,11 @@ namespace {
 
 constexpr int kFwd = 0, kDx = 1, kDw = 2;
 constexpr int kHalf = 128;   // output rows, and B columns, of one CTA of the pair
-constexpr int kTile = 256;   // output tile: rows and columns
+constexpr int kTile = 256;   // output tile: rows, and columns at most
 constexpr int kStepK = 64;   // inner dimension per stage: one 128-byte swizzle atom
 constexpr int kBoxBytes = 64 * 64 * 2;  // a 64-column box of 64 rows
 constexpr uint32_t kTmemCols = 512;     // two accumulators of 256 columns
-constexpr int kWarps = 8;
+constexpr int kWarps = 12;
 
 constexpr int kStages = 7;
 constexpr int kABytes = kHalf * kStepK * 2;
@@ -109,6 +109,7 @@ struct Args {
   typename JobsOf<MODE>::type j;
   int32_t T, K, N;
   int32_t n_steps;         // steps of the inner dimension (forward, dx)
+  int32_t width;           // columns of a tile: 256, 128 or 64
   int32_t col_tiles;       // column tiles of the output
   int32_t nb;              // column tiles per block of the traversal
   const uint8_t* tok_mod;
@@ -244,7 +245,10 @@ struct RunWalk {
 template <int ACT>
 __device__ __forceinline__ void act32(float (&v)[32]) {
 #pragma unroll
-  for (int e = 0; e < 32; ++e) v[e] = act_fwd<ACT>(v[e]);
+  for (int e = 0; e < 32; e += 2) {
+    const uint64_t r = act_fwd2<ACT>(f2_pack(v[e], v[e + 1]));
+    f2_unpack(r, v[e], v[e + 1]);
+  }
 }
 
 // 32 columns of one accumulator row; the caller masks what it stores.
@@ -283,67 +287,66 @@ __device__ __forceinline__ void store32(mf_bf16* p, int left, const float (&f)[3
     }
 }
 
-// The forward's epilogue on one row of a 256-column tile: bias, the kept
-// pre-activation, activation, residual. With an 8-bit checkpoint the row's 128
-// values of a block are read twice from TMEM, once for their largest magnitude;
-// z itself never reaches memory.
+// The forward's epilogue on columns [cc0, cc1) of one row of a tile (a block of
+// scales at most): bias, the kept pre-activation, activation, residual. With an
+// 8-bit checkpoint the row's values of the block are read twice from TMEM, once for
+// their largest magnitude; z itself never reaches memory.
 __device__ __forceinline__ void forward_row(const Args<kFwd>& a, uint32_t taddr, int t, int m,
-                                            bool keep, int n0) {
+                                            bool keep, int n0, int cc0, int cc1) {
   const LinearEpilogue& ep = a.ep;
   const size_t rowoff = static_cast<size_t>(t) * a.N;
   const float* bias = ep.bias == nullptr ? nullptr : ep.bias + static_cast<size_t>(m) * a.N;
+  if (n0 + cc1 > a.N) cc1 = a.N - n0;
+  float s = 0.f, inv = 0.f;
+  uint32_t mask = 0;
+  if (ep.z8 != nullptr && cc0 < cc1) {
+    uint32_t top = 0;
 #pragma unroll 1
-  for (int blk = 0; blk < kTile; blk += kAct8Block) {
-    if (n0 + blk >= a.N) break;
-    float s = 0.f, inv = 0.f;
-    if (ep.z8 != nullptr) {
-      uint32_t top = 0;
-#pragma unroll 1
-      for (int cc = blk; cc < blk + kAct8Block; cc += 32) {
-        const int left = a.N - n0 - cc;
-        if (left <= 0) break;
-        float f[32];
-        acc_load32(taddr + cc, f);
-        if (bias != nullptr) add_bias32(bias + n0 + cc, left, f);
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (e < left) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
-      }
-      act8_scale(__uint_as_float(top), s, inv);
-      if (keep)
-        ep.z_scale[static_cast<size_t>(t) * ((a.N + kAct8Block - 1) / kAct8Block) +
-                   (n0 + blk) / kAct8Block] = s;
-    }
-#pragma unroll 1
-    for (int cc = blk; cc < blk + kAct8Block; cc += 32) {
-      const int c0 = n0 + cc, left = a.N - c0;
-      if (left <= 0) break;
+    for (int cc = cc0; cc < cc1; cc += 32) {
       float f[32];
       acc_load32(taddr + cc, f);
-      if (bias != nullptr) add_bias32(bias + c0, left, f);
-      if (ep.z8 != nullptr && keep) {
+      if (bias != nullptr) add_bias32(bias + n0 + cc, cc1 - cc, f);
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (e < cc1 - cc) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
+    }
+    act8_scale(__uint_as_float(top), s, inv);
+    mask = inv == 0.f ? 0u : 0xFFFFFFFFu;
+    if (keep)
+      ep.z_scale[static_cast<size_t>(t) * ((a.N + kAct8Block - 1) / kAct8Block) +
+                 (n0 + cc0) / kAct8Block] = s;
+  }
+#pragma unroll 1
+  for (int cc = cc0; cc < cc1; cc += 32) {
+    const int c0 = n0 + cc, left = cc1 - cc;
+    float f[32];
+    acc_load32(taddr + cc, f);
+    if (bias != nullptr) add_bias32(bias + c0, left, f);
+    if (ep.z8 != nullptr && keep) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q * 8 < left)
+          __stcs(reinterpret_cast<uint2*>(ep.z8 + rowoff + c0) + q,
+                 make_uint2(act8_code4(f2_pack(f[8 * q], f[8 * q + 1]),
+                                       f2_pack(f[8 * q + 2], f[8 * q + 3]), inv, mask),
+                            act8_code4(f2_pack(f[8 * q + 4], f[8 * q + 5]),
+                                       f2_pack(f[8 * q + 6], f[8 * q + 7]), inv, mask)));
+    }
+    if (ep.z != nullptr && keep) store32(ep.z + rowoff + c0, left, f);
+    if (ep.act == MF_ACT_GELU) act32<MF_ACT_GELU>(f);
+    if (ep.act == MF_ACT_SILU) act32<MF_ACT_SILU>(f);
+    if (keep) {
+      if (ep.resid != nullptr) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (q * 8 < left)
-            __stcs(reinterpret_cast<uint2*>(ep.z8 + rowoff + c0) + q,
-                   make_uint2(act8_code4(f + 8 * q, inv), act8_code4(f + 8 * q + 4, inv)));
-      }
-      if (ep.z != nullptr && keep) store32(ep.z + rowoff + c0, left, f);
-      if (ep.act == MF_ACT_GELU) act32<MF_ACT_GELU>(f);
-      if (ep.act == MF_ACT_SILU) act32<MF_ACT_SILU>(f);
-      if (keep) {
-        if (ep.resid != nullptr) {
+          if (q * 8 < left) {
+            float r[8];
+            bf16x8_unpack(*(reinterpret_cast<const uint4*>(ep.resid + rowoff + c0) + q), r);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (q * 8 < left) {
-              float r[8];
-              bf16x8_unpack(*(reinterpret_cast<const uint4*>(ep.resid + rowoff + c0) + q), r);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) f[8 * q + e] += r[e];
-            }
-        }
-        store32(ep.out + rowoff + c0, left, f);
+            for (int e = 0; e < 8; ++e) f[8 * q + e] += r[e];
+          }
       }
+      store32(ep.out + rowoff + c0, left, f);
     }
   }
 }
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(&bars[i], i < kFull + kStages ? 2u : i == kAccEmpty || i == kAccEmpty + 1 ? 8u : 1u);
+      mbar_init(&bars[i], i < kFull + kStages ? 2u : i == kAccEmpty || i == kAccEmpty + 1 ? 16u : 1u);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_map(&map_a);
@@ -401,6 +404,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t keep = keep_in_l2();
+      // This CTA's half of a tile's B columns. A strided B comes in two boxes of 64
+      // columns whatever the width; the MMA reads what the width says.
+      const int half = args.width / 2;
+      const uint32_t bytes = kABytes + (MODE == kFwd ? half * kStepK * 2 : kABytes);
       uint32_t it = 0, part_uses = 0;  // bit st: parity of PART[st]'s uses
       uint32_t part_used = 0;          // bit st: used at all
       bool ok = true;
@@ -423,7 +430,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           uint8_t* sa = smem + st * kStageBytes;
           uint8_t* sb = sa + kABytes;
           if constexpr (MODE == kDw) {
-            const int xa = w.nt * kTile + rank * kHalf, xb = w.kt * kTile + rank * kHalf;
+            const int xa = w.nt * kTile + rank * kHalf, xb = w.kt * args.width + rank * half;
             if (walk.left < kStepK) {
               mbar_expect_tx(&bars[kPart + st], kStageBytes);
               tma_load_2d(sa, &map_a, &bars[kPart + st], xa, walk.row);
@@ -442,9 +449,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             }
             walk.next(args, w.m);
           } else {
-            const int row = blk * kTile + rank * kHalf, col = ct * kTile + rank * kHalf;
+            const int row = blk * kTile + rank * kHalf, col = ct * args.width + rank * half;
             const uint32_t bar = cluster_addr(&bars[kFull + st], 0);
-            expect_pair(bar, kStageBytes);
+            expect_pair(bar, bytes);
             tma_load_2d_pair(sa, &map_a, bar, s * kStepK, row);
             if constexpr (MODE == kFwd) {
               load_w(sb, &map_b, bar, s * kStepK, col, m, keep);
@@ -470,7 +477,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       constexpr int A_MN = MODE == kDw, B_MN = MODE != kFwd;
-      constexpr uint32_t IDESC = idesc_bf16_f32(2 * kHalf, kTile, A_MN, B_MN);
+      const uint32_t IDESC = idesc_bf16_f32(2 * kHalf, args.width, A_MN, B_MN);
       // a 16-element step is 32 bytes along a contiguous inner dimension, 16 rows
       // of 128 bytes along a strided one
       constexpr uint64_t A_STEP = A_MN ? 128 : 2, B_STEP = B_MN ? 128 : 2;
@@ -523,27 +530,50 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
     __syncwarp();
   } else if (warp >= 4) {
+    // A warp reaches the 32 TMEM lanes of its number modulo 4; warps 4..7 take the
+    // tile's columns up to 128, warps 8..11 the rest.
     const int wq = warp & 3;
     const int row = wq * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+    const int cc0 = warp >= 8 ? kTile / 2 : 0;
+    const int cc1 = warp >= 8 ? args.width : min(kTile / 2, args.width);
     uint32_t ul = 0;
     for (int u = unit0; u < units; u += stride, ++ul) {
       const uint32_t acc = ul & 1;
       if (!warp_wait(&bars[kAccFull + acc], (ul >> 1) & 1, args.ctl, abort_flag)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + lane_base + acc * kTile;
-      if constexpr (MODE == kDw) {
-        const DwUnit w = dw_unit(args, u);
-        const int n = w.nt * kTile + rank * kHalf + row, k0 = w.kt * kTile;
-        const bool keep = n < args.N;
-        mf_bf16* out = args.ep.out + (static_cast<size_t>(w.m) * args.N + n) * args.K + k0;
-        float* part = w.slot < 0 ? nullptr
-                                 : args.j.part + (static_cast<size_t>(w.slot) * kTile +
-                                                  rank * kHalf + row) * kTile;
+      if constexpr (MODE == kFwd) {
+        int blk = 0, m = 0, ct = 0;
+        row_job(u, blk, m, ct);
+        const int t = blk * kTile + rank * kHalf + row;
+        const bool keep = t < args.T && __ldg(args.tok_mod + t) == m;
+        forward_row(args, taddr, t, m, keep, ct * args.width, cc0, cc1);
+      } else {
+        int k0;
+        bool keep;
+        mf_bf16* out;
+        float* part = nullptr;
+        if constexpr (MODE == kDw) {
+          const DwUnit w = dw_unit(args, u);
+          const int n = w.nt * kTile + rank * kHalf + row;
+          k0 = w.kt * args.width;
+          keep = n < args.N;
+          out = args.ep.out + (static_cast<size_t>(w.m) * args.N + n) * args.K + k0;
+          if (w.slot >= 0)
+            part = args.j.part +
+                   (static_cast<size_t>(w.slot) * kTile + rank * kHalf + row) * kTile;
+        } else {
+          int blk = 0, m = 0, ct = 0;
+          row_job(u, blk, m, ct);
+          const int t = blk * kTile + rank * kHalf + row;
+          k0 = ct * args.width;
+          keep = t < args.T && __ldg(args.tok_mod + t) == m;
+          out = args.ep.out + static_cast<size_t>(t) * args.K + k0;
+        }
+        const int end = min(cc1, args.K - k0);
 #pragma unroll 1
-        for (int cc = 0; cc < kTile; cc += 32) {
-          const int left = args.K - k0 - cc;
-          if (left <= 0) break;
+        for (int cc = cc0; cc < end; cc += 32) {
           float f[32];
           acc_load32(taddr + cc, f);
           if (part != nullptr) {
@@ -552,26 +582,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
               *(reinterpret_cast<float4*>(part + cc) + q) =
                   make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
           } else if (keep) {
-            store32(out + cc, left, f);
-          }
-        }
-      } else {
-        int blk = 0, m = 0, ct = 0;
-        row_job(u, blk, m, ct);
-        const int t = blk * kTile + rank * kHalf + row;
-        const bool keep = t < args.T && __ldg(args.tok_mod + t) == m;
-        if constexpr (MODE == kFwd) {
-          forward_row(args, taddr, t, m, keep, ct * kTile);
-        } else {
-          const int k0 = ct * kTile;
-          mf_bf16* out = args.ep.out + static_cast<size_t>(t) * args.K + k0;
-#pragma unroll 1
-          for (int cc = 0; cc < kTile; cc += 32) {
-            const int left = args.K - k0 - cc;
-            if (left <= 0) break;
-            float f[32];
-            acc_load32(taddr + cc, f);
-            if (keep) store32(out + cc, left, f);
+            store32(out + cc, end - cc, f);
           }
         }
       }
@@ -660,9 +671,9 @@ __global__ void __launch_bounds__(256) dz_kernel(const mf_bf16* __restrict__ dou
   const bool on = c < N;
   const int nb = (N + kAct8Block - 1) / kAct8Block;
   const int r0 = blockIdx.x * kDzRows, r1 = min(T, r0 + kDzRows);
-  float sum[2][8];
+  uint64_t sum[2][4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sum[0][e] = sum[1][e] = 0.f;
+  for (int e = 0; e < 4; ++e) sum[0][e] = sum[1][e] = 0;
   for (int t0 = r0 + rl; t0 < r1; t0 += 8 * kDzUnroll) {
     uint4 vd[kDzUnroll], vz[kDzUnroll];
     float vs[kDzUnroll];
@@ -691,26 +702,28 @@ __global__ void __launch_bounds__(256) dz_kernel(const mf_bf16* __restrict__ dou
     for (int u = 0; u < kDzUnroll; ++u) {
       const int t = t0 + u * 8;
       if (t >= r1 || !on) continue;
-      float d[8];
-      bf16x8_unpack(vd[u], d);
+      uint64_t d[4];
+      bf16x8_f2(vd[u], d);
       if constexpr (ACT != MF_ACT_NONE) {
-        float f[8];
+        uint64_t f[4];
         if constexpr (Z8)
           act8_load(make_uint2(vz[u].x, vz[u].y), vs[u], f);
         else
-          bf16x8_unpack(vz[u], f);
+          bf16x8_f2(vz[u], f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] *= act_grad<ACT>(f[e]);
-        *reinterpret_cast<uint4*>(dz + static_cast<size_t>(t) * N + c) = bf16x8_pack(d);
+        for (int e = 0; e < 4; ++e) d[e] = f2_mul(d[e], act_grad2<ACT>(f[e]));
+        *reinterpret_cast<uint4*>(dz + static_cast<size_t>(t) * N + c) = f2_bf16x8(d);
       }
       if (mod[u] > 1) {
         atomicCAS(ctl.err, 0, static_cast<int>(MF_ERR_INVALID));
         continue;
       }
+      if (mod[u] == 0) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sum[0][e] += mod[u] == 0 ? d[e] : 0.f;
-        sum[1][e] += mod[u] == 1 ? d[e] : 0.f;
+        for (int e = 0; e < 4; ++e) sum[0][e] = f2_add(sum[0][e], d[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[1][e] = f2_add(sum[1][e], d[e]);
       }
     }
   }
@@ -718,7 +731,8 @@ __global__ void __launch_bounds__(256) dz_kernel(const mf_bf16* __restrict__ dou
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[m][rl][cl * 8 + e] = sum[m][e];
+    for (int e = 0; e < 4; ++e)
+      f2_unpack(sum[m][e], acc[m][rl][cl * 8 + 2 * e], acc[m][rl][cl * 8 + 2 * e + 1]);
   __syncthreads();
   const int col = blockIdx.y * 256 + threadIdx.x;
   if (col < N) {
@@ -851,12 +865,26 @@ void row_jobs(const TokenRuns& runs, int32_t T, GemmJobs* jobs) {
       if (has[b] & (1u << m)) jobs->job[jobs->n++] = static_cast<uint16_t>(b | (m << 15));
 }
 
+// Width of the column tiles: 256, or 128 or 64 while all tiles then still fit one
+// round over the pairs of SMs (short packs, small layers: the epilogue, which no next
+// tile's MMAs hide there, shrinks with the width). Filling the last of several rounds
+// by other widths did not pay: at 8464 x 3072 x 12288 width 240 runs 22.5 rounds'
+// worth instead of 23 and takes 502 us instead of 483, the copies of A growing and
+// the halves leaving the 64-column atoms.
+int tile_width(int rows, int cols, int pairs, int least) {
+  int w = kTile;
+  while (w / 2 >= least && rows * ((cols + w / 2 - 1) / (w / 2)) <= pairs) w /= 2;
+  return w;
+}
+
 template <int MODE>
-void fill(Args<MODE>& a, int32_t T, int32_t K, int32_t N, int cols, const KernelCtl& ctl) {
+void fill(Args<MODE>& a, int32_t T, int32_t K, int32_t N, int cols, int width,
+          const KernelCtl& ctl) {
   a.T = T;
   a.K = K;
   a.N = N;
-  a.col_tiles = tiles_of(cols);
+  a.width = width;
+  a.col_tiles = (cols + width - 1) / width;
   a.nb = a.col_tiles < 12 ? a.col_tiles : 12;
   a.ctl = ctl;
 }
@@ -910,13 +938,13 @@ bool token_runs(const mf_sample_desc* desc, int32_t S, TokenRuns* runs, int32_t*
 cudaError_t launch_linear_fused(const mf_bf16* x, const mf_bf16* W, const TokenRuns& runs,
                                 const uint8_t* tok_mod, int32_t T, int32_t K, int32_t N,
                                 const LinearEpilogue& ep, const KernelCtl& ctl, cudaStream_t st) {
-  CUtensorMap ma, mb;
-  if (!make_map(&ma, x, K, T, 0, kHalf) ||
-      !make_map(&mb, W, K, N, 2, kHalf))
-    return cudaErrorInvalidValue;
   static thread_local Args<kFwd> a;
-  fill(a, T, K, N, N, ctl);
   row_jobs(runs, T, &a.j.jobs);
+  fill(a, T, K, N, N, tile_width(a.j.jobs.n, N, max_clusters<kFwd>(),
+                                    ep.z8 != nullptr ? kAct8Block : 64), ctl);
+  CUtensorMap ma, mb;
+  if (!make_map(&ma, x, K, T, 0, kHalf) || !make_map(&mb, W, K, N, 2, a.width / 2))
+    return cudaErrorInvalidValue;
   a.n_steps = (K + kStepK - 1) / kStepK;
   a.tok_mod = tok_mod;
   a.ep = ep;
@@ -972,8 +1000,8 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
         !make_map(&mb, b.W, K, N, 2, kStepK))
       return cudaErrorInvalidValue;
     static thread_local Args<kDx> a;
-    fill(a, T, K, N, K, ctl);
     row_jobs(runs, T, &a.j.jobs);
+    fill(a, T, K, N, K, tile_width(a.j.jobs.n, K, max_clusters<kDx>(), 64), ctl);
     a.n_steps = (N + kStepK - 1) / kStepK;
     a.tok_mod = b.tok_mod;
     a.ep = LinearEpilogue{};
@@ -997,7 +1025,7 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
     if (!make_map(&ma, dz, N, T, 0, kStepK) || !make_map(&mb, x, K, T, 0, kStepK))
       return cudaErrorInvalidValue;
     static thread_local Args<kDw> a;
-    fill(a, T, K, N, K, ctl);
+    fill(a, T, K, N, K, kTile, ctl);
     a.ep = LinearEpilogue{};
     a.ep.out = b.dW;
     a.j.part = dw_part;

@@ -85,10 +85,11 @@ def test_largest_magnitudes():
     q, s = _quantize(x)
     assert int(q[0, 0]) == 127 and np.isfinite(host(s)).all()
     y = torch.empty((1, 128), dtype=torch.bfloat16, device="cuda")
-    for act, want in ((mf.MF_ACT_GELU, 0.0), (mf.MF_ACT_SILU, 0.0)):
+    for act in (mf.MF_ACT_GELU, mf.MF_ACT_SILU):
         mf.mf_act8_dequantize(q, s, 1, 128, act, y)
         y1 = host(y)
-        assert (y1[0, 1::2] == want).all() and (y1[0, ::2] > 1e38).all()
+        # far below 0 the activation is held where it is within 1e-16 of its limit 0
+        assert (np.abs(y1[0, 1::2]) <= 1e-16).all() and (y1[0, ::2] > 1e38).all()
 
 
 def test_empty():
