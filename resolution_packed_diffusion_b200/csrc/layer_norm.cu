@@ -32,6 +32,7 @@
 
 #include "act8.cuh"
 #include "mlp_internal.h"
+#include "pdl.cuh"
 
 namespace mf {
 
@@ -333,11 +334,12 @@ constexpr int kBwdRows = 2;  // rows per group and step: an even number, so that
                              // step's 8-bit codes start on a 16-byte boundary
 constexpr int kMaxStages = 4;
 
-// part: [grid][2 modalities][2 (dgamma, dbeta)][hid], or dgamma and dbeta themselves
-// when the grid is one CTA (part NULL). Dynamic shared memory: the stages, then, with
+// A thread owns CH chunks of eight channels, a.lanes chunks apart. part:
+// [grid][2 modalities][2 (dgamma, dbeta)][hid], or dgamma and dbeta themselves when
+// the grid is one CTA (part NULL). Dynamic shared memory: the stages, then, with
 // more than one group, [groups][2][2][hid] fp32. One group adds into its place in
 // memory directly: each column has one owner.
-template <int SUB, int THREADS, int PER_SM, bool X8>
+template <int SUB, int CH, int THREADS, int PER_SM, bool X8>
 __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
     const mf_bf16* __restrict__ dy, const mf_bf16* __restrict__ x, const Act8 x8,
     const float* __restrict__ gamma, const float2* __restrict__ stats, const mf_bf16* resid,
@@ -350,16 +352,18 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
   const int group = threadIdx.x / a.lanes, gl = threadIdx.x - group * a.lanes;
-  const int warps = a.lanes / 32;
-  const int c = gl * 8;
-  const bool on = c < a.hid;
+  const int warps = a.lanes / 32, lane = threadIdx.x & 31;
+  bool on[CH];
+#pragma unroll
+  for (int j = 0; j < CH; ++j) on[j] = (gl + j * a.lanes) * 8 < a.hid;
   const float inv_n = 1.f / static_cast<float>(a.hid);
   const int nb = (a.hid + kAct8Block - 1) / kAct8Block;
   int r0, r1;
   cta_rows<R>(a, r0, r1);
   const int step = a.groups * R;
   const int steps = (r1 - r0 + step - 1) / step;
-  float* cols = reinterpret_cast<float*>(smem + sg.stages * sg.bytes());
+  const int stage_bytes = sg.bytes();
+  float* cols = reinterpret_cast<float*>(smem + sg.stages * stage_bytes);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < sg.stages; ++i) mbar_init(&full[i], 1);
@@ -367,11 +371,11 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
     fence_mbar_init();
   }
   __syncthreads();
-  // thread 0: the rows of step s into its stage
-  auto issue = [&](int s) {
+  // thread 0: the rows of step s into stage `at`
+  auto issue = [&](int s, int at) {
     const int row = r0 + s * step, rows = min(step, r1 - row);
-    uint8_t* dst = smem + (s % sg.stages) * sg.bytes();
-    uint64_t* bar = &full[s % sg.stages];
+    uint8_t* dst = smem + at * stage_bytes;
+    uint64_t* bar = &full[at];
     const size_t off = static_cast<size_t>(row) * a.hid;
     const uint32_t n = static_cast<uint32_t>(rows) * a.hid;
     uint32_t nx = 2 * n;
@@ -391,67 +395,87 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
     if (resid != nullptr) bulk_load(dst + sg.x + sg.d, resid + off, 2 * n, bar);
   };
   if (threadIdx.x == 0)
-    for (int s = 0; s < sg.stages && s < steps; ++s) issue(s);
+    for (int s = 0; s < sg.stages && s < steps; ++s) issue(s, s);
+  pdl_release();
 
-  uint64_t gam[4], ag[4], ab[4];
+  uint64_t gam[CH][4], ag[CH][4], ab[CH][4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) gam[e] = ag[e] = ab[e] = 0;
+  for (int j = 0; j < CH; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) gam[j][e] = ag[j][e] = ab[j][e] = 0;
   int cm = -1, seen = 0;
   // this group's place for modality m: dgamma's row, dbeta's row
   auto place = [&](int m, float*& g, float*& b) {
     if (a.groups > 1) {
-      g = cols + (static_cast<size_t>(group) * 4 + m * 2) * a.hid + c;
+      g = cols + (static_cast<size_t>(group) * 4 + m * 2) * a.hid;
       b = g + a.hid;
     } else if (part != nullptr) {
-      g = part + (static_cast<size_t>(blockIdx.x) * 4 + m * 2) * a.hid + c;
+      g = part + (static_cast<size_t>(blockIdx.x) * 4 + m * 2) * a.hid;
       b = g + a.hid;
     } else {
-      g = dgamma + static_cast<size_t>(m) * a.hid + c;
-      b = dbeta + static_cast<size_t>(m) * a.hid + c;
+      g = dgamma + static_cast<size_t>(m) * a.hid;
+      b = dbeta + static_cast<size_t>(m) * a.hid;
     }
   };
   auto flush = [&]() {
-    if (on && cm >= 0) {
-      float *g, *b;
-      place(cm, g, b);
-      const bool more = (seen >> cm) & 1;
-      uint64_t* g2 = reinterpret_cast<uint64_t*>(g);
-      uint64_t* b2 = reinterpret_cast<uint64_t*>(b);
+    if (cm < 0) return;
+    float *g, *b;
+    place(cm, g, b);
+    const bool more = (seen >> cm) & 1;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      if (!on[j]) continue;
+      uint64_t* g2 = reinterpret_cast<uint64_t*>(g + (gl + j * a.lanes) * 8);
+      uint64_t* b2 = reinterpret_cast<uint64_t*>(b + (gl + j * a.lanes) * 8);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        g2[e] = more ? f2_add(g2[e], ag[e]) : ag[e];
-        b2[e] = more ? f2_add(b2[e], ab[e]) : ab[e];
-        ag[e] = ab[e] = 0;
+        g2[e] = more ? f2_add(g2[e], ag[j][e]) : ag[j][e];
+        b2[e] = more ? f2_add(b2[e], ab[j][e]) : ab[j][e];
+        ag[j][e] = ab[j][e] = 0;
       }
-      seen |= 1 << cm;
     }
+    seen |= 1 << cm;
   };
   // small per-row values of a step, fetched one step ahead
   float2 nst[R];
-  float nsc[R];
+  float nsc[R][CH];
   int nmod[R];
   auto fetch = [&](int row) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const bool live = row + i < r1;
-      nmod[i] = live ? __ldg(a.tok_mod + row + i) : -1;
-      nst[i] = live ? __ldg(stats + row + i) : make_float2(0.f, 0.f);
-      nsc[i] = 0.f;
-      if constexpr (X8)
-        if (live && on)
-          nsc[i] = __ldg(x8.scale + static_cast<size_t>(row + i) * nb + c / kAct8Block);
+      nmod[i] = -1;
+      nst[i] = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < CH; ++j) nsc[i][j] = 0.f;
+      if (row + i < r1) {
+        nmod[i] = __ldg(a.tok_mod + row + i);
+        nst[i] = __ldg(stats + row + i);
+        if constexpr (X8) {
+          const float* sc = x8.scale + static_cast<size_t>(row + i) * nb;
+#pragma unroll
+          for (int j = 0; j < CH; ++j)
+            if (on[j]) nsc[i][j] = __ldg(sc + (gl + j * a.lanes) * 8 / kAct8Block);
+        }
+      }
     }
   };
-  fetch(r0 + group * R);
-  for (int s = 0; s < steps; ++s) {
-    const int row = r0 + s * step + group * R;
-    float2 st[R];  // (mean * rstd, rstd)
-    float sc[R];
+  int row = r0 + group * R;
+  const uint32_t elem = static_cast<uint32_t>(group * R) * a.hid + gl * 8;  // within a stage
+  const uint32_t chunk = a.lanes * 8;
+  mf_bf16* out = dx + static_cast<size_t>(row) * a.hid + gl * 8;
+  const size_t out_step = static_cast<size_t>(step) * a.hid;
+  int at = 0, prev = 0;
+  uint32_t parity = 0;
+  fetch(row);
+  for (int s = 0; s < steps; ++s, row += step, out += out_step) {
+    float2 st[R];  // (-mean * rstd, rstd)
+    float sc[R][CH];
     int mod[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      st[i] = make_float2(nst[i].x * nst[i].y, nst[i].y);
-      sc[i] = nsc[i];
+      st[i] = make_float2(-nst[i].x * nst[i].y, nst[i].y);
+#pragma unroll
+      for (int j = 0; j < CH; ++j) sc[i][j] = nsc[i][j];
       mod[i] = nmod[i];
       if (mod[i] > 1) {
         if (gl == 0) atomicCAS(a.ctl.err, 0, static_cast<int>(MF_ERR_INVALID));
@@ -459,20 +483,21 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
       }
     }
     fetch(row + step);
-    const uint8_t* sx = smem + (s % sg.stages) * sg.bytes();
-    const uint8_t* sd = sx + sg.x;
+    const uint8_t* sx = smem + at * stage_bytes;
+    const uint8_t* sd = sx + sg.x + 2 * elem;
     const uint8_t* sr = sd + sg.d;
+    sx += X8 ? elem : 2 * elem;
     // A wait that runs out is recorded and the step goes on, so that every thread
     // still meets every barrier.
-    (void)mbar_wait(&full[s % sg.stages], (s / sg.stages) & 1, a.ctl, abort_flag);
-    auto operands = [&](int i, uint64_t (&h)[4], uint64_t (&d)[4]) {
-      const uint32_t at = static_cast<uint32_t>(group * R + i) * a.hid + c;
+    (void)mbar_wait(&full[at], parity, a.ctl, abort_flag);
+    auto operands = [&](int i, int j, uint64_t (&h)[4], uint64_t (&d)[4]) {
+      const uint32_t o = i * a.hid + j * chunk;
       if constexpr (X8)
-        act8_load(*reinterpret_cast<const uint2*>(sx + at), sc[i], h);
+        act8_load(*reinterpret_cast<const uint2*>(sx + o), sc[i][j], h);
       else
-        bf16x8_f2(*reinterpret_cast<const uint4*>(sx + 2 * at), h);
-      bf16x8_f2(*reinterpret_cast<const uint4*>(sd + 2 * at), d);
-      const uint64_t r2 = f2_both(st[i].y), m2 = f2_both(-st[i].x);
+        bf16x8_f2(*reinterpret_cast<const uint4*>(sx + 2 * o), h);
+      bf16x8_f2(*reinterpret_cast<const uint4*>(sd + 2 * o), d);
+      const uint64_t r2 = f2_both(st[i].y), m2 = f2_both(st[i].x);
 #pragma unroll
       for (int e = 0; e < 4; ++e) h[e] = f2_fma(h[e], r2, m2);
     };
@@ -484,29 +509,34 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
       if (mod[i] != cm) {
         flush();
         cm = mod[i];
-        if (on) load8_f2(gamma + static_cast<size_t>(cm) * a.hid + c, gam);
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+          if (on[j])
+            load8_f2(gamma + static_cast<size_t>(cm) * a.hid + (gl + j * a.lanes) * 8, gam[j]);
       }
-      if (on) {
-        uint64_t h[4], d[4], s1 = 0, s2 = 0;
-        operands(i, h, d);
+      uint64_t s1 = 0, s2 = 0;
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        if (!on[j]) continue;
+        uint64_t h[4], d[4];
+        operands(i, j, h, d);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          ag[e] = f2_fma(d[e], h[e], ag[e]);
-          ab[e] = f2_add(ab[e], d[e]);
-          const uint64_t g = f2_mul(d[e], gam[e]);
+          ag[j][e] = f2_fma(d[e], h[e], ag[j][e]);
+          ab[j][e] = f2_add(ab[j][e], d[e]);
+          const uint64_t g = f2_mul(d[e], gam[j][e]);
           s1 = f2_add(s1, g);
           s2 = f2_fma(g, h[e], s2);
         }
-        float lo, hi;
-        f2_unpack(s1, lo, hi);
-        sums[2 * i] = lo + hi;
-        f2_unpack(s2, lo, hi);
-        sums[2 * i + 1] = lo + hi;
       }
+      float lo, hi;
+      f2_unpack(s1, lo, hi);
+      sums[2 * i] = lo + hi;
+      f2_unpack(s2, lo, hi);
+      sums[2 * i + 1] = lo + hi;
     }
     // The four sums over a group's lanes. Lane l ends with sum l mod 4: two rounds
     // that halve the sums a lane holds, then plain ones (6 shuffles in place of 20).
-    const int lane = threadIdx.x & 31;
     float part4;
     {
       const bool odd = lane & 1, upper = lane & 2;
@@ -522,7 +552,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
     if (SUB == 32 && warps > 1 && lane < 4) red[s & 1][threadIdx.x >> 5][lane] = part4;
     __syncthreads();
     // every thread has left the previous step, so its stage can be filled again
-    if (threadIdx.x == 0 && s > 0 && s - 1 + sg.stages < steps) issue(s - 1 + sg.stages);
+    if (threadIdx.x == 0 && s > 0 && s - 1 + sg.stages < steps) issue(s - 1 + sg.stages, prev);
     if (SUB == 32 && warps > 1) {
       // sum l mod 4 of the group's warps, eight of them at a time
       part4 = 0.f;
@@ -530,44 +560,51 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) part4 += __shfl_xor_sync(0xffffffffu, part4, o);
     }
+    part4 *= -inv_n;
 #pragma unroll
-    for (int i = 0; i < 2 * R; ++i)
-      sums[i] = __shfl_sync(0xffffffffu, part4, (lane & ~3) | i) * inv_n;
-    if (!on) continue;
-    uint64_t gm[4];
-    int gmod = cm;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) gm[e] = gam[e];
-#pragma unroll
-    for (int i = R - 1; i >= 0; --i) {
-      if (mod[i] < 0) continue;
-      if (mod[i] != gmod) {  // an earlier row of the step, before the change
-        gmod = mod[i];
-        load8_f2(gamma + static_cast<size_t>(gmod) * a.hid + c, gm);
-      }
-      uint64_t h[4], d[4], o[4] = {0, 0, 0, 0};
-      operands(i, h, d);
-      if (resid != nullptr)
-        bf16x8_f2(*reinterpret_cast<const uint4*>(
-                      sr + 2 * (static_cast<uint32_t>(group * R + i) * a.hid + c)), o);
-      const uint64_t m1 = f2_both(-sums[2 * i]), m2 = f2_both(-sums[2 * i + 1]);
+    for (int i = 0; i < 2 * R; ++i) sums[i] = __shfl_sync(0xffffffffu, part4, (lane & ~3) | i);
+    // `other`: a row before the step's change of modality, its weights read again
+    auto finish = [&](int i, bool other) {
+      const uint64_t m1 = f2_both(sums[2 * i]), m2 = f2_both(sums[2 * i + 1]);
       const uint64_t r2 = f2_both(st[i].y);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        o[e] = f2_fma(f2_fma(h[e], m2, f2_fma(d[e], gm[e], m1)), r2, o[e]);
-      *reinterpret_cast<uint4*>(dx + static_cast<size_t>(row + i) * a.hid + c) = f2_bf16x8(o);
+      for (int j = 0; j < CH; ++j) {
+        if (!on[j]) continue;
+        uint64_t h[4], d[4], w[4], o[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = gam[j][e];
+        if (other)
+          load8_f2(gamma + static_cast<size_t>(mod[i]) * a.hid + (gl + j * a.lanes) * 8, w);
+        operands(i, j, h, d);
+        if (resid != nullptr)
+          bf16x8_f2(*reinterpret_cast<const uint4*>(sr + 2 * (i * a.hid + j * chunk)), o);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          o[e] = f2_fma(f2_fma(h[e], m2, f2_fma(d[e], w[e], m1)), r2, o[e]);
+        *reinterpret_cast<uint4*>(out + static_cast<size_t>(i) * a.hid + j * chunk) = f2_bf16x8(o);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (mod[i] >= 0) finish(i, mod[i] != cm);
+    prev = at;
+    if (++at == sg.stages) {
+      at = 0;
+      parity ^= 1;
     }
   }
   flush();
-  if (on) {  // a modality that this group did not meet
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      if ((seen >> m) & 1) continue;
-      float *g, *b;
-      place(m, g, b);
+  for (int m = 0; m < 2; ++m) {  // a modality that this group did not meet
+    if ((seen >> m) & 1) continue;
+    float *g, *b;
+    place(m, g, b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] = b[e] = 0.f;
-    }
+    for (int j = 0; j < CH; ++j)
+      if (on[j])
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          g[(gl + j * a.lanes) * 8 + e] = b[(gl + j * a.lanes) * 8 + e] = 0.f;
   }
   if (a.groups == 1) return;
   __syncthreads();
@@ -585,23 +622,28 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
 }
 
 // dgamma / dbeta = the sum over the n partials, in a fixed order: 32 columns per
-// CTA, eight slices of the partials each, then the slices in order.
-__global__ void __launch_bounds__(256) ln_cols_kernel(const float* __restrict__ part, int n,
-                                                      int hid, float* __restrict__ dgamma,
-                                                      float* __restrict__ dbeta) {
-  __shared__ float s[8][32];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
+// CTA, 32 slices of the partials, one warp each, then the slices in order.
+__global__ void __launch_bounds__(1024) ln_cols_kernel(const float* __restrict__ part, int n,
+                                                       int hid, float* __restrict__ dgamma,
+                                                       float* __restrict__ dbeta) {
+  __shared__ float s[32][33];
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
+  pdl_wait();
   float v = 0.f;
   if (col < 4 * hid) {
-#pragma unroll 8
-    for (int k = slice; k < n; k += 8) v += __ldg(part + static_cast<size_t>(k) * 4 * hid + col);
+#pragma unroll 10
+    for (int k = slice; k < n; k += 32) v += __ldcg(part + static_cast<size_t>(k) * 4 * hid + col);
   }
-  s[slice][threadIdx.x & 31] = v;
+  s[slice][lane] = v;
   __syncthreads();
-  if (slice == 0 && col < 4 * hid) {
+  // warp w: columns w, 32 slices by shuffles
+  v = s[lane][slice];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) v += s[k][threadIdx.x & 31];
-    const int m = col / (2 * hid), r = col - m * 2 * hid;
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int c = blockIdx.x * 32 + slice;
+  if (lane == 0 && c < 4 * hid) {
+    const int m = c / (2 * hid), r = c - m * 2 * hid;
     (r < hid ? dgamma : dbeta)[m * hid + (r < hid ? r : r - hid)] = v;
   }
 }
@@ -633,9 +675,20 @@ cudaError_t fwd_rows(const mf_bf16* x, const float* gamma, const float* beta, co
   return cudaGetLastError();
 }
 
-// CTAs per SM of the backward: two of up to 512 threads, so that one computes while
-// the other waits at its barrier.
-int bwd_per_sm(int threads) { return threads > 512 ? 1 : 2; }
+// How the backward shares rows: as the forward up to 2048 channels, then two chunks
+// per thread, which halves what a row costs beside its values.
+RowShape bwd_row_shape(int32_t hid) {
+  if (hid <= 2048) return row_shape(hid);
+  RowShape s;
+  s.lanes = (hid / 8 + 63) / 64 * 32;
+  s.groups = 1;
+  s.threads = s.lanes;
+  return s;
+}
+
+// CTAs per SM: several, so that one computes while another waits at its barrier; one
+// above 256 threads, whose registers leave no more room.
+int bwd_per_sm(const RowShape& s) { return s.threads > 256 ? 1 : s.groups > 1 || s.threads > 128 ? 2 : 3; }
 
 BwdStage bwd_stage(const RowShape& s, int32_t hid, bool x8, bool resid) {
   auto round128 = [](int v) { return (v + 127) / 128 * 128; };
@@ -645,32 +698,39 @@ BwdStage bwd_stage(const RowShape& s, int32_t hid, bool x8, bool resid) {
   g.d = round128(2 * n);
   g.r = resid ? g.d : 0;
   const int cols = s.groups > 1 ? s.groups * 16 * hid : 0;
-  const int room = (bwd_per_sm(s.threads) == 2 ? 110 : 220) * 1024 - cols;
+  const int room = 222 * 1024 / bwd_per_sm(s) - 2048 - cols;
   g.stages = room / g.bytes();
   if (g.stages > kMaxStages) g.stages = kMaxStages;
   return g;
 }
 
-template <int SUB, int THREADS, int PER_SM, bool X8>
+// One CTA per step up to one per SM, then whole multiples of eight steps: each CTA
+// leaves column sums for the second kernel to add.
+int bwd_grid(const RowShape& s, int32_t T) {
+  const int steps = (T + s.groups * kBwdRows - 1) / (s.groups * kBwdRows), sms = ln_sms();
+  if (steps <= sms) return steps;
+  const int by_steps = steps / 8, cap = sms * bwd_per_sm(s);
+  return by_steps < sms ? sms : by_steps < cap ? by_steps : cap;
+}
+
+template <int SUB, int CH, int THREADS, int PER_SM, bool X8>
 cudaError_t bwd_shape(const mf_bf16* dy, const mf_bf16* x, const Act8& x8, const float* gamma,
                       const float* stats, const mf_bf16* resid, const LnArgs& a, const RowShape& s,
                       mf_bf16* dx, float* dgamma, float* dbeta, float* part, cudaStream_t st) {
-  auto kernel = layer_norm_bwd_kernel<SUB, THREADS, PER_SM, X8>;
+  auto kernel = layer_norm_bwd_kernel<SUB, CH, THREADS, PER_SM, X8>;
   const BwdStage g = bwd_stage(s, a.hid, X8, resid != nullptr);
   const int smem = g.stages * g.bytes() + (s.groups > 1 ? s.groups * 16 * a.hid : 0);
   const cudaError_t ae =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (ae != cudaSuccess) return ae;
-  const int steps = (a.T + a.groups * kBwdRows - 1) / (a.groups * kBwdRows);
-  const int cap = ln_sms() * bwd_per_sm(s.threads);
-  const int grid = steps < cap ? steps : cap;
+  const int grid = bwd_grid(s, a.T);
   float* p = grid > 1 ? part : nullptr;
   kernel<<<grid, s.threads, smem, st>>>(dy, x, x8, gamma, reinterpret_cast<const float2*>(stats),
                                         resid, a, g, dx, p, dgamma, dbeta);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p == nullptr) return e;
-  ln_cols_kernel<<<(4 * a.hid + 31) / 32, 256, 0, st>>>(p, grid, a.hid, dgamma, dbeta);
-  return cudaGetLastError();
+  return launch_dependent(ln_cols_kernel, dim3((4 * a.hid + 31) / 32), dim3(1024), 0, st, p, grid,
+                          a.hid, dgamma, dbeta);
 }
 
 }  // namespace
@@ -692,8 +752,7 @@ cudaError_t launch_layer_norm(const mf_bf16* x, const float* gamma, const float*
 }
 
 size_t layer_norm_bwd_ws(int32_t T, int32_t hid) {
-  (void)T;
-  return static_cast<size_t>(ln_sms()) * bwd_per_sm(row_shape(hid).threads) * 4 * hid * sizeof(float);
+  return static_cast<size_t>(bwd_grid(bwd_row_shape(hid), T)) * 4 * hid * sizeof(float);
 }
 
 cudaError_t launch_layer_norm_bwd(const mf_bf16* dy, const mf_bf16* x, const Act8& x8,
@@ -701,20 +760,21 @@ cudaError_t launch_layer_norm_bwd(const mf_bf16* dy, const mf_bf16* x, const Act
                                   const mf_bf16* resid, int32_t T, int32_t hid, mf_bf16* dx,
                                   float* dgamma, float* dbeta, void* ws, const KernelCtl& ctl,
                                   cudaStream_t st) {
-  const RowShape s = row_shape(hid);
+  const RowShape s = bwd_row_shape(hid);
   const LnArgs a{tok_mod, T, hid, s.lanes, s.groups, ctl};
   float* part = reinterpret_cast<float*>(ws);
-#define MF_LN_BWD(SUB, THREADS, PER_SM)                                                        \
-  (x8.q != nullptr                                                                             \
-       ? bwd_shape<SUB, THREADS, PER_SM, true>(dy, x, x8, gamma, stats, resid, a, s, dx, dgamma, \
-                                               dbeta, part, st)                                \
-       : bwd_shape<SUB, THREADS, PER_SM, false>(dy, x, x8, gamma, stats, resid, a, s, dx, dgamma, \
-                                                dbeta, part, st))
-  if (s.lanes == 8) return MF_LN_BWD(8, 256, 2);
-  if (s.lanes == 16) return MF_LN_BWD(16, 256, 2);
-  if (s.threads <= 384) return MF_LN_BWD(32, 384, 2);
-  if (s.threads <= 512) return MF_LN_BWD(32, 512, 2);
-  return MF_LN_BWD(32, 1024, 1);
+#define MF_LN_BWD(SUB, CH, THREADS, PER_SM)                                                  \
+  (x8.q != nullptr                                                                           \
+       ? bwd_shape<SUB, CH, THREADS, PER_SM, true>(dy, x, x8, gamma, stats, resid, a, s, dx, \
+                                                   dgamma, dbeta, part, st)                  \
+       : bwd_shape<SUB, CH, THREADS, PER_SM, false>(dy, x, x8, gamma, stats, resid, a, s, dx, \
+                                                    dgamma, dbeta, part, st))
+  if (s.lanes == 8) return MF_LN_BWD(8, 1, 256, 2);
+  if (s.lanes == 16) return MF_LN_BWD(16, 1, 256, 2);
+  if (hid <= 2048) return MF_LN_BWD(32, 1, 256, 2);
+  if (hid <= 3072) return MF_LN_BWD(32, 2, 192, 2);
+  if (hid <= 4096) return MF_LN_BWD(32, 2, 256, 2);
+  return MF_LN_BWD(32, 2, 512, 1);
 #undef MF_LN_BWD
 }
 
