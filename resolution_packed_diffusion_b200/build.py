@@ -25,7 +25,7 @@ LIB = os.path.join(PKG, "libmf.so")
 
 SOURCES = ["mf_api.cu", "elementwise.cu", "attn_fwd.cu", "noalloc.cu", "gemm.cu", "mmdit.cu",
            "attn_bwd.cu", "block_bwd.cu", "vae.cu", "mmdit_bwd.cu", "act8.cu", "layer_norm.cu",
-           "linear_fused.cu"]
+           "linear_fused.cu", "linear_rows.cu"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -1,0 +1,55 @@
+// linear_common.cuh -- what the two kernels of the fused linear layer share: tensor
+// maps, the bounded drain, TMEM reads.
+#pragma once
+
+#include <cuda.h>
+
+#include <cstdint>
+
+#include "act8.cuh"
+#include "mf_ptx.cuh"
+#include "mlp_internal.h"
+
+namespace mf {
+
+// L2 policy of the weights, which every row block reads again.
+__device__ __forceinline__ uint64_t keep_in_l2() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > limit_ns) return;
+}
+
+// 32 columns of one accumulator row; the caller masks what it stores.
+__device__ __forceinline__ void acc_load32(uint32_t taddr, float (&f)[32]) {
+  uint32_t v[32];
+  tmem_ld32(taddr, v);
+  tmem_ld_wait();
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    asm volatile("" : "+r"(v[e]));
+    f[e] = __uint_as_float(v[e]);
+  }
+}
+
+// [sets][rows][cols] bf16 with boxes of 64 columns x box_rows, 128-byte swizzle; what
+// lies outside reads as zeros. sets 0: a two-dimensional map.
+bool linear_map(CUtensorMap* map, const mf_bf16* base, int64_t cols, int64_t rows, int sets,
+                int box_rows);
+
+// Few rows (linear_rows.cu): the forward, and dx. false: not for this shape.
+constexpr int kFewRows = 128;
+inline bool few_rows(int32_t T) { return T <= kFewRows; }
+cudaError_t launch_linear_rows(const mf_bf16* x, const mf_bf16* W, const TokenRuns& runs,
+                               const uint8_t* tok_mod, int32_t T, int32_t K, int32_t N,
+                               const LinearEpilogue& ep, const KernelCtl& ctl, cudaStream_t st);
+cudaError_t launch_linear_rows_dx(const mf_bf16* dz, const mf_bf16* W, const TokenRuns& runs,
+                                  const uint8_t* tok_mod, int32_t T, int32_t K, int32_t N,
+                                  mf_bf16* dx, const KernelCtl& ctl, cudaStream_t st);
+
+}  // namespace mf

@@ -43,6 +43,7 @@
 
 #include "act8.cuh"
 #include "gemm_internal.h"
+#include "linear_common.cuh"
 #include "mf_internal.h"
 #include "mf_ptx.cuh"
 #include "mlp_internal.h"
@@ -147,21 +148,9 @@ __device__ __forceinline__ void load_w(void* dst, const CUtensorMap* map, uint32
       : "memory");
 }
 
-__device__ __forceinline__ uint64_t keep_in_l2() {
-  uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
-  return p;
-}
-
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const KernelCtl& ctl,
                                           volatile int* abort_flag) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl, abort_flag));
-}
-
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity))
-    if (globaltimer_ns() - t0 > limit_ns) return;
 }
 
 // mbar_wait for arrivals of both CTAs that release writes to their shared memory:
@@ -248,18 +237,6 @@ __device__ __forceinline__ void act32(float (&v)[32]) {
   for (int e = 0; e < 32; e += 2) {
     const uint64_t r = act_fwd2<ACT>(f2_pack(v[e], v[e + 1]));
     f2_unpack(r, v[e], v[e + 1]);
-  }
-}
-
-// 32 columns of one accumulator row; the caller masks what it stores.
-__device__ __forceinline__ void acc_load32(uint32_t taddr, float (&f)[32]) {
-  uint32_t v[32];
-  tmem_ld32(taddr, v);
-  tmem_ld_wait();
-#pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    asm volatile("" : "+r"(v[e]));
-    f[e] = __uint_as_float(v[e]);
   }
 }
 
@@ -784,23 +761,6 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// [sets][rows][cols] bf16 with boxes of 64 columns x box_rows, 128-byte swizzle; what
-// lies outside reads as zeros. sets 0: a two-dimensional map.
-bool make_map(CUtensorMap* map, const mf_bf16* base, int64_t cols, int64_t rows, int sets,
-              int box_rows) {
-  const EncodeTiledFn enc = encode_fn();
-  if (enc == nullptr) return false;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
-                              static_cast<cuuint64_t>(sets)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols * 2),
-                                 static_cast<cuuint64_t>(cols * rows * 2)};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, sets > 0 ? 3 : 2, const_cast<mf_bf16*>(base),
-             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int MODE>
 cudaLaunchConfig_t config(int clusters, cudaLaunchAttribute* attr, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
@@ -904,6 +864,21 @@ size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
+bool linear_map(CUtensorMap* map, const mf_bf16* base, int64_t cols, int64_t rows, int sets,
+                int box_rows) {
+  const EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(sets)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols * 2),
+                                 static_cast<cuuint64_t>(cols * rows * 2)};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, sets > 0 ? 3 : 2, const_cast<mf_bf16*>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool token_runs(const mf_sample_desc* desc, int32_t S, TokenRuns* runs, int32_t* T) {
   memset(runs->n, 0, sizeof(runs->n));
   memset(runs->count, 0, sizeof(runs->count));
@@ -938,12 +913,13 @@ bool token_runs(const mf_sample_desc* desc, int32_t S, TokenRuns* runs, int32_t*
 cudaError_t launch_linear_fused(const mf_bf16* x, const mf_bf16* W, const TokenRuns& runs,
                                 const uint8_t* tok_mod, int32_t T, int32_t K, int32_t N,
                                 const LinearEpilogue& ep, const KernelCtl& ctl, cudaStream_t st) {
+  if (few_rows(T)) return launch_linear_rows(x, W, runs, tok_mod, T, K, N, ep, ctl, st);
   static thread_local Args<kFwd> a;
   row_jobs(runs, T, &a.j.jobs);
   fill(a, T, K, N, N, tile_width(a.j.jobs.n, N, max_clusters<kFwd>(),
                                     ep.z8 != nullptr ? kAct8Block : 64), ctl);
   CUtensorMap ma, mb;
-  if (!make_map(&ma, x, K, T, 0, kHalf) || !make_map(&mb, W, K, N, 2, a.width / 2))
+  if (!linear_map(&ma, x, K, T, 0, kHalf) || !linear_map(&mb, W, K, N, 2, a.width / 2))
     return cudaErrorInvalidValue;
   a.n_steps = (K + kStepK - 1) / kStepK;
   a.tok_mod = tok_mod;
@@ -994,10 +970,13 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
     }
   }
 
-  if (b.dx != nullptr) {
+  if (b.dx != nullptr && few_rows(T)) {
+    e = launch_linear_rows_dx(dz, b.W, runs, b.tok_mod, T, K, N, b.dx, ctl, st);
+    if (e != cudaSuccess) return e;
+  } else if (b.dx != nullptr) {
     CUtensorMap ma, mb;
-    if (!make_map(&ma, dz, N, T, 0, kHalf) ||
-        !make_map(&mb, b.W, K, N, 2, kStepK))
+    if (!linear_map(&ma, dz, N, T, 0, kHalf) ||
+        !linear_map(&mb, b.W, K, N, 2, kStepK))
       return cudaErrorInvalidValue;
     static thread_local Args<kDx> a;
     row_jobs(runs, T, &a.j.jobs);
@@ -1022,7 +1001,7 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
       x = x_ws;
     }
     CUtensorMap ma, mb;
-    if (!make_map(&ma, dz, N, T, 0, kStepK) || !make_map(&mb, x, K, T, 0, kStepK))
+    if (!linear_map(&ma, dz, N, T, 0, kStepK) || !linear_map(&mb, x, K, T, 0, kStepK))
       return cudaErrorInvalidValue;
     static thread_local Args<kDw> a;
     fill(a, T, K, N, K, kTile, ctl);

@@ -22,7 +22,13 @@ CASES = [(((0, 0, 0, 1),), 8, 8), (((1, 1, 1, 0),), 64, 256), (((1, 1, 1, 1),), 
          (MIXED, 200, 248), (((1, 8, 16, 128), (1, 16, 8, 128)), 128, 256),
          (((0, 0, 0, 300), (1, 11, 13, 0)), 320, 256), (((0, 0, 0, 65),), 1000, 136),
          (((1, 25, 41, 0),), 264, 328), (((1, 16, 16, 20), (1, 8, 32, 12)), 512, 128),
-         (tuple((1, 1, 3, 2) for _ in range(60)), 96, 304), (((1, 5, 13, 2), (1, 31, 9, 70)), 1040, 776)]
+         (tuple((1, 1, 3, 2) for _ in range(60)), 96, 304), (((1, 5, 13, 2), (1, 31, 9, 70)), 1040, 776),
+         # few rows: both modalities, every padding of the tokens, inner dimensions that
+         # are cut over 1 to 8 CTAs and end inside a step, outputs that end inside a tile
+         (((1, 3, 5, 2), (0, 0, 0, 7)), 1032, 392), (((1, 8, 8, 64),), 2048, 136),
+         (((0, 0, 0, 33), (1, 3, 9, 1)), 4096, 1000), (((0, 0, 0, 1),), 4096, 2048),
+         (((1, 2, 2, 4), (1, 1, 1, 1)), 328, 5128), (((1, 7, 17, 8),), 64, 1024),
+         (((0, 0, 0, 129),), 512, 256)]
 
 
 def _data(descs, K, N, seed):
