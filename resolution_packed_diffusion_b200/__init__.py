@@ -498,7 +498,7 @@ def mf_linear_fused(x, W, bias, resid, tok_mod, descs, K: int, N: int, act: int,
     the pre-activation. ``descs`` as for mf_modality_linear, or a make_descs array."""
     arr, S = _descs(descs)
     _check(lib.mf_linear_fused(_ptr(x), _ptr(W), _ptr(bias), _ptr(resid), _ptr(tok_mod),
-                               ctypes.cast(arr, _P), S, K, N, act, _ptr(z), _ptr(z8),
+                               arr, S, K, N, act, _ptr(z), _ptr(z8),
                                _ptr(z_scale), _ptr(out), _stream(stream)), "mf_linear_fused")
 
 
@@ -512,6 +512,6 @@ def mf_linear_fused_bwd(dout, x, x8, x_scale, W, z, z8, z_scale, tok_mod, descs,
     or (x8, x_scale), the pre-activation z or (z8, z_scale)."""
     arr, S = _descs(descs)
     _check(lib.mf_linear_fused_bwd(_ptr(dout), _ptr(x), _ptr(x8), _ptr(x_scale), _ptr(W), _ptr(z),
-                                   _ptr(z8), _ptr(z_scale), _ptr(tok_mod), ctypes.cast(arr, _P), S,
+                                   _ptr(z8), _ptr(z_scale), _ptr(tok_mod), arr, S,
                                    K, N, act, _ptr(dx), _ptr(dW), _ptr(db), _ptr(workspace),
                                    ws_bytes, _stream(stream)), "mf_linear_fused_bwd")

@@ -20,15 +20,16 @@
 
 #include "act8.cuh"
 #include "mlp_internal.h"
+#include "pdl.cuh"
 
 namespace mf {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
-constexpr int kLanes = kAct8Block / 8;           // lanes of a block
-constexpr int kPerCta = kThreads / kLanes;       // blocks a CTA takes per step
+constexpr int kThreads = kAct8Threads;
+constexpr int kUnroll = kAct8Unroll;
+constexpr int kLanes = kAct8Lanes;
+constexpr int kPerCta = kAct8PerCta;
 
 // Largest |x| of eight bf16 values as a 15-bit pattern (NaN above infinity).
 __device__ __forceinline__ uint32_t absmax_bits(const uint4& u) {
@@ -42,6 +43,8 @@ __global__ void __launch_bounds__(kThreads) act8_quantize_kernel(const mf_bf16* 
                                                                  int64_t items, int nb, int C,
                                                                  int8_t* __restrict__ q,
                                                                  float* __restrict__ scale) {
+  pdl_wait();
+  pdl_release();
   const int lane = threadIdx.x % kLanes;
   const int64_t base = blockIdx.x * static_cast<int64_t>(kPerCta * kUnroll) + threadIdx.x / kLanes;
   uint4 v[kUnroll];
@@ -79,34 +82,9 @@ __global__ void __launch_bounds__(kThreads) act8_dequantize_kernel(const int8_t*
                                                                    const float* __restrict__ scale,
                                                                    int64_t items, int nb, int C,
                                                                    mf_bf16* __restrict__ y) {
-  const int lane = threadIdx.x % kLanes;
-  const int64_t base = blockIdx.x * static_cast<int64_t>(kPerCta * kUnroll) + threadIdx.x / kLanes;
-  uint2 v[kUnroll];
-  float s[kUnroll];
-  int64_t off[kUnroll];
-  bool in[kUnroll];
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t item = base + u * kPerCta;
-    const int64_t row = item / nb;
-    const int c = static_cast<int>(item - row * nb) * kAct8Block + lane * 8;
-    in[u] = item < items && c < C;
-    off[u] = row * C + c;
-    v[u] = in[u] ? __ldcs(reinterpret_cast<const uint2*>(q + off[u])) : make_uint2(0, 0);
-    s[u] = item < items ? __ldg(scale + item) : 0.f;
-  }
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    uint64_t f[4];
-    act8_load(v[u], s[u], f);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = act_fwd2<ACT>(f[e]);
-    if (in[u]) __stcs(reinterpret_cast<uint4*>(y + off[u]), f2_bf16x8(f));
-  }
-}
-
-unsigned grid_of(int64_t items) {
-  return static_cast<unsigned>((items + kPerCta * kUnroll - 1) / (kPerCta * kUnroll));
+  pdl_wait();
+  pdl_release();
+  act8_decode<ACT>(q, scale, items, nb, C, y, blockIdx.x);
 }
 
 }  // namespace
@@ -116,22 +94,23 @@ cudaError_t launch_act8_quantize(const mf_bf16* x, int32_t T, int32_t C, int8_t*
                                  cudaStream_t st) {
   const int nb = act8_blocks(C);
   const int64_t items = static_cast<int64_t>(T) * nb;
-  act8_quantize_kernel<<<grid_of(items), kThreads, 0, st>>>(x, items, nb, C, q, scale);
-  return cudaGetLastError();
+  return launch_dependent(act8_quantize_kernel, dim3(act8_decode_blocks(items)), dim3(kThreads), 0,
+                          st, x, items, nb, C, q, scale);
 }
 
 cudaError_t launch_act8_dequantize(const int8_t* q, const float* scale, int32_t T, int32_t C,
                                    int32_t act, mf_bf16* y, cudaStream_t st) {
   const int nb = act8_blocks(C);
   const int64_t items = static_cast<int64_t>(T) * nb;
-  const unsigned grid = grid_of(items);
+  const dim3 grid(act8_decode_blocks(items)), block(kThreads);
   if (act == MF_ACT_GELU)
-    act8_dequantize_kernel<MF_ACT_GELU><<<grid, kThreads, 0, st>>>(q, scale, items, nb, C, y);
-  else if (act == MF_ACT_SILU)
-    act8_dequantize_kernel<MF_ACT_SILU><<<grid, kThreads, 0, st>>>(q, scale, items, nb, C, y);
-  else
-    act8_dequantize_kernel<MF_ACT_NONE><<<grid, kThreads, 0, st>>>(q, scale, items, nb, C, y);
-  return cudaGetLastError();
+    return launch_dependent(act8_dequantize_kernel<MF_ACT_GELU>, grid, block, 0, st, q, scale,
+                            items, nb, C, y);
+  if (act == MF_ACT_SILU)
+    return launch_dependent(act8_dequantize_kernel<MF_ACT_SILU>, grid, block, 0, st, q, scale,
+                            items, nb, C, y);
+  return launch_dependent(act8_dequantize_kernel<MF_ACT_NONE>, grid, block, 0, st, q, scale, items,
+                          nb, C, y);
 }
 
 }  // namespace mf

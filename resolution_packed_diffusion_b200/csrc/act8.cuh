@@ -172,4 +172,45 @@ __device__ __forceinline__ uint64_t act_grad2(uint64_t z) {
   return f2_fma(zd, f2_fma(f2_mul(s, f2_both(-1.f)), s, s), s);
 }
 
+// One CTA's share (256 threads) of y = act(q s): blocks of 128 channels, sixteen
+// lanes each, kAct8Unroll of them per thread with all loads issued first.
+constexpr int kAct8Threads = 256;
+constexpr int kAct8Unroll = 4;
+constexpr int kAct8Lanes = kAct8Block / 8;
+constexpr int kAct8PerCta = kAct8Threads / kAct8Lanes;  // blocks a CTA takes per step
+
+inline unsigned act8_decode_blocks(int64_t items) {
+  return static_cast<unsigned>((items + kAct8PerCta * kAct8Unroll - 1) / (kAct8PerCta * kAct8Unroll));
+}
+
+template <int ACT>
+__device__ __forceinline__ void act8_decode(const int8_t* __restrict__ q,
+                                            const float* __restrict__ scale, int64_t items, int nb,
+                                            int C, mf_bf16* __restrict__ y, int64_t block) {
+  const int lane = threadIdx.x % kAct8Lanes;
+  const int64_t base = block * (kAct8PerCta * kAct8Unroll) + threadIdx.x / kAct8Lanes;
+  uint2 v[kAct8Unroll];
+  float s[kAct8Unroll];
+  int64_t off[kAct8Unroll];
+  bool in[kAct8Unroll];
+#pragma unroll
+  for (int u = 0; u < kAct8Unroll; ++u) {
+    const int64_t item = base + u * kAct8PerCta;
+    const int64_t row = item / nb;
+    const int c = static_cast<int>(item - row * nb) * kAct8Block + lane * 8;
+    in[u] = item < items && c < C;
+    off[u] = row * C + c;
+    v[u] = in[u] ? __ldcs(reinterpret_cast<const uint2*>(q + off[u])) : make_uint2(0, 0);
+    s[u] = item < items ? __ldg(scale + item) : 0.f;
+  }
+#pragma unroll
+  for (int u = 0; u < kAct8Unroll; ++u) {
+    uint64_t f[4];
+    act8_load(v[u], s[u], f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = act_fwd2<ACT>(f[e]);
+    if (in[u]) __stcs(reinterpret_cast<uint4*>(y + off[u]), f2_bf16x8(f));
+  }
+}
+
 }  // namespace mf

@@ -150,6 +150,8 @@ __global__ void __launch_bounds__(THREADS) layer_norm_kernel(const mf_bf16* __re
   cta_rows<R>(a, r0, r1);
   float gam[8], bet[8];
   int cm = -1;
+  pdl_wait();
+  pdl_release();
   uint4 next[R];
   int mod_next[R];
   auto fetch = [&](int row) {
@@ -252,6 +254,8 @@ __global__ void __launch_bounds__(row_warps(NCH) * 32, 1)
   constexpr int kRowWarps = row_warps(NCH);
   const int row0 = blockIdx.x * kRowWarps + warp, stride = gridDim.x * kRowWarps;
   uint4 v[NCH];
+  pdl_wait();
+  pdl_release();
   for (int i = threadIdx.x; i < 8 * nc; i += blockDim.x) {
     // i: ((modality * 2 + which) * 2 + half) * nc + chunk
     const int chunk = i % nc, r = i / nc;
@@ -371,6 +375,8 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
     fence_mbar_init();
   }
   __syncthreads();
+  pdl_wait();
+  pdl_release();
   // thread 0: the rows of step s into stage `at`
   auto issue = [&](int s, int at) {
     const int row = r0 + s * step, rows = min(step, r1 - row);
@@ -396,7 +402,6 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
   };
   if (threadIdx.x == 0)
     for (int s = 0; s < sg.stages && s < steps; ++s) issue(s, s);
-  pdl_release();
 
   uint64_t gam[CH][4], ag[CH][4], ab[CH][4];
 #pragma unroll
@@ -630,6 +635,7 @@ __global__ void __launch_bounds__(1024) ln_cols_kernel(const float* __restrict__
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   pdl_wait();
+  pdl_release();
   float v = 0.f;
   if (col < 4 * hid) {
 #pragma unroll 10
@@ -653,9 +659,9 @@ cudaError_t fwd_shape(const mf_bf16* x, const float* gamma, const float* beta, c
                       int threads, float eps, mf_bf16* y, float* stats, cudaStream_t st) {
   const int steps = (a.T + a.groups * R - 1) / (a.groups * R);
   const int cap = ln_sms() * (threads > 512 ? 1 : threads > 256 ? 2 : 4);
-  layer_norm_kernel<SUB, R, THREADS><<<steps < cap ? steps : cap, threads, 0, st>>>(
-      x, gamma, beta, a, eps, y, reinterpret_cast<float2*>(stats));
-  return cudaGetLastError();
+  return launch_dependent(layer_norm_kernel<SUB, R, THREADS>, dim3(steps < cap ? steps : cap),
+                          dim3(threads), 0, st, x, gamma, beta, a, eps, y,
+                          reinterpret_cast<float2*>(stats));
 }
 
 template <int NCH>
@@ -670,9 +676,8 @@ cudaError_t fwd_rows(const mf_bf16* x, const float* gamma, const float* beta, co
   }
   constexpr int kRowWarps = row_warps(NCH);
   const int need = (a.T + kRowWarps - 1) / kRowWarps, cap = ln_sms();
-  kernel<<<need < cap ? need : cap, kRowWarps * 32, smem, st>>>(x, gamma, beta, a, eps, y,
-                                                                reinterpret_cast<float2*>(stats));
-  return cudaGetLastError();
+  return launch_dependent(kernel, dim3(need < cap ? need : cap), dim3(kRowWarps * 32), smem, st, x,
+                          gamma, beta, a, eps, y, reinterpret_cast<float2*>(stats));
 }
 
 // How the backward shares rows: as the forward up to 2048 channels, then two chunks
@@ -725,9 +730,9 @@ cudaError_t bwd_shape(const mf_bf16* dy, const mf_bf16* x, const Act8& x8, const
   if (ae != cudaSuccess) return ae;
   const int grid = bwd_grid(s, a.T);
   float* p = grid > 1 ? part : nullptr;
-  kernel<<<grid, s.threads, smem, st>>>(dy, x, x8, gamma, reinterpret_cast<const float2*>(stats),
-                                        resid, a, g, dx, p, dgamma, dbeta);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      launch_dependent(kernel, dim3(grid), dim3(s.threads), smem, st, dy, x, x8, gamma,
+                       reinterpret_cast<const float2*>(stats), resid, a, g, dx, p, dgamma, dbeta);
   if (e != cudaSuccess || p == nullptr) return e;
   return launch_dependent(ln_cols_kernel, dim3((4 * a.hid + 31) / 32), dim3(1024), 0, st, p, grid,
                           a.hid, dgamma, dbeta);

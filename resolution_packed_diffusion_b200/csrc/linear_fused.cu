@@ -32,6 +32,7 @@
 //   warp 0      TMA producer (one lane)
 //   warp 1      tcgen05 issuer (one lane of the leader CTA)
 //   warp 2      dW only: zeroes the rows past a run
+//   warp 3      dx or dW: adds the partial sums of db that dz_kernel left
 //   warps 4..11 epilogue, from the accumulator that the MMAs have left for the other
 //               one of the two: one output row and half of the columns per thread
 // Every wait is bounded.
@@ -47,6 +48,7 @@
 #include "mf_internal.h"
 #include "mf_ptx.cuh"
 #include "mlp_internal.h"
+#include "pdl.cuh"
 
 namespace mf {
 
@@ -91,9 +93,16 @@ struct RunJobs {
   int32_t start[2][MF_MAX_SAMPLES];
   int32_t len[2][MF_MAX_SAMPLES];
   int32_t it0[2][MF_MAX_SAMPLES + 1];
-  int32_t units[2];   // output tiles x splits of the modality (0: no tokens)
+  int32_t units[2];   // output tiles x splits of the modality
   int32_t splits[2];  // parts of the modality's steps
   float* part;        // [units of split modalities][256][256], or NULL
+};
+
+// out[c] = the sum of part[k][c] over k, in order.
+struct ColumnSums {
+  const float* part;
+  int32_t n, cols;
+  float* out;
 };
 
 template <int MODE>
@@ -115,6 +124,7 @@ struct Args {
   int32_t nb;              // column tiles per block of the traversal
   const uint8_t* tok_mod;
   LinearEpilogue ep;       // forward: all of it; dx and dW: out
+  ColumnSums db;           // dx and dW: db's partials, or out NULL
   KernelCtl ctl;
 };
 
@@ -358,6 +368,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   cluster_sync();  // both CTAs' barriers exist before either reaches the other's
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_release();
   const int rank = static_cast<int>(cluster_ctarank());
   const int unit0 = static_cast<int>(blockIdx.x >> 1);
   const int stride = static_cast<int>(gridDim.x >> 1);
@@ -381,10 +393,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t keep = keep_in_l2();
-      // This CTA's half of a tile's B columns. A strided B comes in two boxes of 64
-      // columns whatever the width; the MMA reads what the width says.
+      // This CTA's half of a tile's B columns; a strided B comes in boxes of 64.
       const int half = args.width / 2;
-      const uint32_t bytes = kABytes + (MODE == kFwd ? half * kStepK * 2 : kABytes);
+      const bool two = half > 64;
+      const uint32_t bytes =
+          kABytes + (MODE == kFwd ? half * kStepK * 2 : two ? 2 * kBoxBytes : kBoxBytes);
       uint32_t it = 0, part_uses = 0;  // bit st: parity of PART[st]'s uses
       uint32_t part_used = 0;          // bit st: used at all
       bool ok = true;
@@ -394,8 +407,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         int blk = 0, m = 0, ct = 0, steps;
         if constexpr (MODE == kDw) {
           w = dw_unit(args, u);
-          walk.start(args, w.m, w.s0);
           steps = w.s1 - w.s0;
+          if (steps > 0) walk.start(args, w.m, w.s0);
         } else {
           row_job(u, blk, m, ct);
           steps = args.n_steps;
@@ -409,20 +422,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           if constexpr (MODE == kDw) {
             const int xa = w.nt * kTile + rank * kHalf, xb = w.kt * args.width + rank * half;
             if (walk.left < kStepK) {
-              mbar_expect_tx(&bars[kPart + st], kStageBytes);
+              mbar_expect_tx(&bars[kPart + st], bytes);
               tma_load_2d(sa, &map_a, &bars[kPart + st], xa, walk.row);
               tma_load_2d(sa + kBoxBytes, &map_a, &bars[kPart + st], xa + 64, walk.row);
               tma_load_2d(sb, &map_b, &bars[kPart + st], xb, walk.row);
-              tma_load_2d(sb + kBoxBytes, &map_b, &bars[kPart + st], xb + 64, walk.row);
+              if (two) tma_load_2d(sb + kBoxBytes, &map_b, &bars[kPart + st], xb + 64, walk.row);
               part_uses ^= 1u << st;
               part_used |= 1u << st;
             } else {
               const uint32_t bar = cluster_addr(&bars[kFull + st], 0);
-              expect_pair(bar, kStageBytes);
+              expect_pair(bar, bytes);
               tma_load_2d_pair(sa, &map_a, bar, xa, walk.row);
               tma_load_2d_pair(sa + kBoxBytes, &map_a, bar, xa + 64, walk.row);
               tma_load_2d_pair(sb, &map_b, bar, xb, walk.row);
-              tma_load_2d_pair(sb + kBoxBytes, &map_b, bar, xb + 64, walk.row);
+              if (two) tma_load_2d_pair(sb + kBoxBytes, &map_b, bar, xb + 64, walk.row);
             }
             walk.next(args, w.m);
           } else {
@@ -434,7 +447,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
               load_w(sb, &map_b, bar, s * kStepK, col, m, keep);
             } else {
               load_w(sb, &map_b, bar, col, s * kStepK, m, keep);
-              load_w(sb + kBoxBytes, &map_b, bar, col + 64, s * kStepK, m, keep);
+              if (two) load_w(sb + kBoxBytes, &map_b, bar, col + 64, s * kStepK, m, keep);
             }
           }
         }
@@ -472,8 +485,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         if constexpr (MODE == kDw) {
           const DwUnit w = dw_unit(args, u);
           m = w.m;
-          walk.start(args, m, w.s0);
           steps = w.s1 - w.s0;
+          if (steps > 0) walk.start(args, m, w.s0);
         } else {
           steps = args.n_steps;
         }
@@ -531,11 +544,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         bool keep;
         mf_bf16* out;
         float* part = nullptr;
+        bool none = false;  // dW of a modality without tokens
         if constexpr (MODE == kDw) {
           const DwUnit w = dw_unit(args, u);
           const int n = w.nt * kTile + rank * kHalf + row;
           k0 = w.kt * args.width;
           keep = n < args.N;
+          none = w.s0 == w.s1;
           out = args.ep.out + (static_cast<size_t>(w.m) * args.N + n) * args.K + k0;
           if (w.slot >= 0)
             part = args.j.part +
@@ -553,6 +568,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         for (int cc = cc0; cc < end; cc += 32) {
           float f[32];
           acc_load32(taddr + cc, f);
+          if (none)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = 0.f;
           if (part != nullptr) {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
@@ -567,12 +585,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars[kAccEmpty + acc], 0));
     }
+  } else if (MODE != kFwd && warp == 3) {
+    if (args.db.out != nullptr) {
+      for (int c = static_cast<int>(blockIdx.x) * 32 + lane; c < args.db.cols;
+           c += static_cast<int>(gridDim.x) * 32) {
+        float v = 0.f;
+#pragma unroll 8
+        for (int k = 0; k < args.db.n; ++k)
+          v += __ldcg(args.db.part + static_cast<size_t>(k) * args.db.cols + c);
+        args.db.out[c] = v;
+      }
+    }
   } else if (MODE == kDw && warp == 2) {
     if constexpr (MODE == kDw) {
       uint32_t it = 0, part_uses = 0;
       bool ok = true;
       for (int u = unit0; u < units && ok; u += stride) {
         const DwUnit w = dw_unit(args, u);
+        if (w.s0 == w.s1) continue;
         RunWalk walk;
         walk.start(args, w.m, w.s0);
         for (int s = w.s0; s < w.s1; ++s, ++it, walk.next(args, w.m)) {
@@ -607,19 +637,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
 // dW[m] = the sum of its parts, in order, rounded once. One thread per 8 columns.
 __global__ void __launch_bounds__(256) dw_parts_kernel(const float* __restrict__ part, int splits,
-                                                       int N, int K, int col_tiles, int tiles,
-                                                       mf_bf16* __restrict__ dW) {
+                                                       int N, int K, int width, int col_tiles,
+                                                       int tiles, mf_bf16* __restrict__ dW) {
+  pdl_wait();
+  pdl_release();
   const int groups = K / 8;
   const int64_t total = static_cast<int64_t>(N) * groups;
   const int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
   if (i < total) {
     const int n = static_cast<int>(i / groups), k = static_cast<int>(i - static_cast<int64_t>(n) * groups) * 8;
-    const float* p = part + ((static_cast<size_t>(n / kTile) * col_tiles + k / kTile) * kTile +
-                             n % kTile) * kTile + k % kTile;
+    const float* p = part + ((static_cast<size_t>(n / kTile) * col_tiles + k / width) * kTile +
+                             n % kTile) * kTile + k % width;
     float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int s = 0; s < splits; ++s, p += static_cast<size_t>(tiles) * kTile * kTile) {
-      const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-      const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(p));
+      const float4 b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
       f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
       f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
     }
@@ -629,25 +661,45 @@ __global__ void __launch_bounds__(256) dw_parts_kernel(const float* __restrict__
 
 // ------------------------------------------------------------ dz and db
 // dz = dout act'(z) (bf16, the operand of both products) and the modality sums of
-// the unrounded dz. A CTA takes kDzRows rows of 256 channels: 32 lanes of eight
+// the unrounded dz. A CTA takes `rows` rows of 256 channels: 32 lanes of eight
 // channels by eight row lanes, four rows of loads in flight per thread; the row
-// lanes' sums meet in shared memory and leave as part[chunk][modality][N], which
-// dz_cols_kernel adds in order. HBM-bound. ACT none: only the sums.
-constexpr int kDzRows = 128;
+// lanes' sums meet in shared memory and leave as part[chunk][modality][N], which a
+// warp of the next product's kernel adds in order (or db itself, when one chunk
+// holds every row). HBM-bound. ACT none: only the sums. The blocks behind these
+// decode an 8-bit x for dW: one launch for both.
 constexpr int kDzUnroll = 4;
+
+// Short packs get short chunks, so that there are CTAs for every SM.
+int dz_rows(int32_t T) { return T <= 2048 ? 32 : T <= 8192 ? 64 : 128; }
+
+struct Decode {
+  Act8 x8;
+  int64_t items;   // blocks of 128 channels; 0: nothing to decode
+  int32_t nb, C;
+  mf_bf16* y;
+};
 
 template <int ACT, bool Z8>
 __global__ void __launch_bounds__(256) dz_kernel(const mf_bf16* __restrict__ dout,
                                                  const mf_bf16* __restrict__ z, const Act8 z8,
                                                  const uint8_t* __restrict__ tok_mod, int T, int N,
+                                                 int rows, int col_blocks, int dz_blocks,
                                                  mf_bf16* __restrict__ dz, float* __restrict__ part,
-                                                 KernelCtl ctl) {
+                                                 const Decode dec, KernelCtl ctl) {
   __shared__ float acc[2][8][256];
+  pdl_wait();
+  pdl_release();
+  if (static_cast<int>(blockIdx.x) >= dz_blocks) {
+    act8_decode<MF_ACT_NONE>(dec.x8.q, dec.x8.scale, dec.items, dec.nb, dec.C, dec.y,
+                             blockIdx.x - dz_blocks);
+    return;
+  }
+  const int chunk = blockIdx.x / col_blocks, cb = blockIdx.x - chunk * col_blocks;
   const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
-  const int c = blockIdx.y * 256 + cl * 8;
+  const int c = cb * 256 + cl * 8;
   const bool on = c < N;
   const int nb = (N + kAct8Block - 1) / kAct8Block;
-  const int r0 = blockIdx.x * kDzRows, r1 = min(T, r0 + kDzRows);
+  const int r0 = chunk * rows, r1 = min(T, r0 + rows);
   uint64_t sum[2][4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) sum[0][e] = sum[1][e] = 0;
@@ -711,35 +763,28 @@ __global__ void __launch_bounds__(256) dz_kernel(const mf_bf16* __restrict__ dou
     for (int e = 0; e < 4; ++e)
       f2_unpack(sum[m][e], acc[m][rl][cl * 8 + 2 * e], acc[m][rl][cl * 8 + 2 * e + 1]);
   __syncthreads();
-  const int col = blockIdx.y * 256 + threadIdx.x;
+  const int col = cb * 256 + threadIdx.x;
   if (col < N) {
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       float v = 0.f;
 #pragma unroll
       for (int r = 0; r < 8; ++r) v += acc[m][r][threadIdx.x];
-      part[(static_cast<size_t>(blockIdx.x) * 2 + m) * N + col] = v;
+      part[(static_cast<size_t>(chunk) * 2 + m) * N + col] = v;
     }
   }
 }
 
-// db = the sum of the chunks' partials in order; 32 columns x 8 slices per CTA.
-__global__ void __launch_bounds__(256) dz_cols_kernel(const float* __restrict__ part, int chunks,
-                                                      int cols, float* __restrict__ db) {
-  __shared__ float s[8][32];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
+// db's partials where no product follows: one thread per column.
+__global__ void __launch_bounds__(128) dz_cols_kernel(const ColumnSums db) {
+  pdl_wait();
+  pdl_release();
+  const int c = blockIdx.x * 128 + threadIdx.x;
+  if (c >= db.cols) return;
   float v = 0.f;
-  if (col < cols) {
-#pragma unroll 4
-    for (int k = slice; k < chunks; k += 8) v += __ldg(part + static_cast<size_t>(k) * cols + col);
-  }
-  s[slice][threadIdx.x & 31] = v;
-  __syncthreads();
-  if (slice == 0 && col < cols) {
-#pragma unroll
-    for (int k = 1; k < 8; ++k) v += s[k][threadIdx.x & 31];
-    db[col] = v;
-  }
+#pragma unroll 8
+  for (int k = 0; k < db.n; ++k) v += __ldcg(db.part + static_cast<size_t>(k) * db.cols + c);
+  db.out[c] = v;
 }
 
 // ------------------------------------------------------------ host side
@@ -772,8 +817,10 @@ cudaLaunchConfig_t config(int clusters, cudaLaunchAttribute* attr, cudaStream_t 
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cfg;
 }
 
@@ -788,8 +835,9 @@ int max_clusters() {
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemBytes) != cudaSuccess)
       return 0;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = config<MODE>(1, attr, nullptr);
+    cfg.numAttrs = 1;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, linear_fused_kernel<MODE>, &cfg) != cudaSuccess)
       return 0;
@@ -803,7 +851,7 @@ cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const A
                            int units, cudaStream_t st) {
   const int mc = max_clusters<MODE>();
   if (mc <= 0) return cudaErrorInvalidConfiguration;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = config<MODE>(units < mc ? units : mc, attr, st);
   return cudaLaunchKernelEx(&cfg, linear_fused_kernel<MODE>, ma, mb, a);
 }
@@ -846,16 +894,25 @@ void fill(Args<MODE>& a, int32_t T, int32_t K, int32_t N, int cols, int width,
   a.width = width;
   a.col_tiles = (cols + width - 1) / width;
   a.nb = a.col_tiles < 12 ? a.col_tiles : 12;
+  a.db = ColumnSums{};
   a.ctl = ctl;
 }
 
 // Pairs of SMs on a B200 (148 SMs): what dW's split and its workspace are sized by.
 constexpr int kPairs = 74;
 
+// Column width of dW's tiles, by the tiles of one modality.
+int dw_width(int32_t K, int32_t N) { return tile_width(tiles_of(N), K, kPairs, 64); }
+int dw_tiles(int32_t K, int32_t N) {
+  const int w = dw_width(K, N);
+  return tiles_of(N) * ((K + w - 1) / w);
+}
+
 // Parts of a modality's steps: one, unless its tiles leave more than half of the
-// pairs without work; then as many as fill them, of at least four steps each.
+// pairs without work; then as many as fill them, of at least 24 steps each (a step
+// takes about 0.35 us, joining the parts about 8 us).
 int dw_splits(int tiles, int steps) {
-  const int by_pairs = kPairs / tiles, by_steps = steps / 4;
+  const int by_pairs = kPairs / tiles, by_steps = steps / 24;
   const int p = by_pairs < by_steps ? by_pairs : by_steps;
   return p > 1 ? p : 1;
 }
@@ -930,12 +987,10 @@ cudaError_t launch_linear_fused(const mf_bf16* x, const mf_bf16* W, const TokenR
 // Workspace, in this order: dz [T][N] bf16; db's partials; an 8-bit x in bf16; dW's
 // parts.
 size_t linear_fused_bwd_ws(int32_t T, int32_t K, int32_t N) {
-  const size_t chunks = static_cast<size_t>((T + kDzRows - 1) / kDzRows);
-  const int tiles = tiles_of(N) * tiles_of(K);
-  const size_t parts = tiles * 2 <= kPairs ? static_cast<size_t>(2) * kPairs : 0;
+  const size_t chunks = static_cast<size_t>((T + dz_rows(T) - 1) / dz_rows(T));
+  const size_t parts = dw_tiles(K, N) * 2 <= kPairs ? static_cast<size_t>(2) * kPairs : 0;
   return round256(static_cast<size_t>(T) * N * 2) + round256(chunks * 2 * N * sizeof(float)) +
-         round256(static_cast<size_t>(T) * K * 2) +
-         parts * kTile * kTile * sizeof(float);
+         round256(static_cast<size_t>(T) * K * 2) + parts * kTile * kTile * sizeof(float);
 }
 
 cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, int32_t T, int32_t K,
@@ -943,7 +998,7 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
   mf_bf16* dz_ws = reinterpret_cast<mf_bf16*>(w);
   w += round256(static_cast<size_t>(T) * N * 2);
-  const int chunks = (T + kDzRows - 1) / kDzRows;
+  const int rows = dz_rows(T), chunks = (T + rows - 1) / rows;
   float* part = reinterpret_cast<float*>(w);
   w += round256(static_cast<size_t>(chunks) * 2 * N * sizeof(float));
   mf_bf16* x_ws = reinterpret_cast<mf_bf16*>(w);
@@ -952,22 +1007,29 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
   cudaError_t e;
 
   const mf_bf16* dz = b.act == MF_ACT_NONE ? b.dout : dz_ws;
-  if (b.act != MF_ACT_NONE || b.db != nullptr) {
-    const dim3 grid(chunks, (N + 255) / 256);
-    float* p = b.db != nullptr ? part : nullptr;
-#define MF_DZ(ACT, Z8) \
-  dz_kernel<ACT, Z8><<<grid, 256, 0, st>>>(b.dout, b.z, b.z8, b.tok_mod, T, N, dz_ws, p, ctl)
-    if (b.act == MF_ACT_NONE) MF_DZ(MF_ACT_NONE, false);
-    else if (b.act == MF_ACT_GELU && b.z8.q != nullptr) MF_DZ(MF_ACT_GELU, true);
-    else if (b.act == MF_ACT_GELU) MF_DZ(MF_ACT_GELU, false);
-    else if (b.z8.q != nullptr) MF_DZ(MF_ACT_SILU, true);
-    else MF_DZ(MF_ACT_SILU, false);
+  ColumnSums db = {part, chunks, 2 * N, chunks > 1 ? b.db : nullptr};
+  // An 8-bit x is decoded once into the workspace (3 bytes of traffic a value, a
+  // tenth of the product's time at 8464 x 12288 x 3072); decoding it between the
+  // copies and the MMAs, again for every 256 output rows, took 2.6 times as long
+  // as the product.
+  Decode dec = {};
+  if (b.dW != nullptr && b.x == nullptr)
+    dec = Decode{b.x8, static_cast<int64_t>(T) * act8_blocks(K), act8_blocks(K), K, x_ws};
+  const int col_blocks = (N + 255) / 256;
+  const int dz_blocks = b.act != MF_ACT_NONE || b.db != nullptr ? chunks * col_blocks : 0;
+  const unsigned blocks = dz_blocks + act8_decode_blocks(dec.items);
+  if (blocks > 0) {
+    float* p = b.db == nullptr ? nullptr : chunks > 1 ? part : b.db;
+#define MF_DZ(ACT, Z8)                                                                           \
+  launch_dependent(dz_kernel<ACT, Z8>, dim3(blocks), dim3(256), 0, st, b.dout, b.z, b.z8,        \
+                   b.tok_mod, T, N, rows, col_blocks, dz_blocks, dz_ws, p, dec, ctl)
+    if (b.act == MF_ACT_NONE) e = MF_DZ(MF_ACT_NONE, false);
+    else if (b.act == MF_ACT_GELU && b.z8.q != nullptr) e = MF_DZ(MF_ACT_GELU, true);
+    else if (b.act == MF_ACT_GELU) e = MF_DZ(MF_ACT_GELU, false);
+    else if (b.z8.q != nullptr) e = MF_DZ(MF_ACT_SILU, true);
+    else e = MF_DZ(MF_ACT_SILU, false);
 #undef MF_DZ
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (b.db != nullptr) {
-      dz_cols_kernel<<<(2 * N + 31) / 32, 256, 0, st>>>(part, chunks, 2 * N, b.db);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
+    if (e != cudaSuccess) return e;
   }
 
   if (b.dx != nullptr && few_rows(T)) {
@@ -985,28 +1047,23 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
     a.tok_mod = b.tok_mod;
     a.ep = LinearEpilogue{};
     a.ep.out = b.dx;
+    a.db = db;
+    db.out = nullptr;
     e = launch_product<kDx>(ma, mb, a, a.j.jobs.n * a.col_tiles, st);
     if (e != cudaSuccess) return e;
   }
 
   if (b.dW != nullptr) {
-    // An 8-bit x is decoded once into the workspace (3 bytes of traffic a value, a
-    // tenth of the product's time at 8464 x 12288 x 3072); decoding it between the
-    // copies and the MMAs, again for every 256 output rows, took 2.6 times as long
-    // as the product.
-    const mf_bf16* x = b.x;
-    if (x == nullptr) {
-      if ((e = launch_act8_dequantize(b.x8.q, b.x8.scale, T, K, MF_ACT_NONE, x_ws, st)) != cudaSuccess)
-        return e;
-      x = x_ws;
-    }
+    const mf_bf16* x = b.x != nullptr ? b.x : x_ws;
     CUtensorMap ma, mb;
     if (!linear_map(&ma, dz, N, T, 0, kStepK) || !linear_map(&mb, x, K, T, 0, kStepK))
       return cudaErrorInvalidValue;
     static thread_local Args<kDw> a;
-    fill(a, T, K, N, K, kTile, ctl);
+    fill(a, T, K, N, K, dw_width(K, N), ctl);
     a.ep = LinearEpilogue{};
     a.ep.out = b.dW;
+    a.db = db;
+    db.out = nullptr;
     a.j.part = dw_part;
     const int tiles = tiles_of(N) * a.col_tiles;
     for (int m = 0; m < 2; ++m) {
@@ -1016,15 +1073,6 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
         a.j.start[m][r] = runs.start[m][r];
         a.j.len[m][r] = runs.len[m][r];
         a.j.it0[m][r + 1] = a.j.it0[m][r] + (runs.len[m][r] + kStepK - 1) / kStepK;
-      }
-      if (runs.count[m] == 0) {
-        const size_t bytes = static_cast<size_t>(N) * K * 2;
-        if ((e = cudaMemsetAsync(reinterpret_cast<uint8_t*>(b.dW) + m * bytes, 0, bytes, st)) !=
-            cudaSuccess)
-          return e;
-        a.j.splits[m] = 1;
-        a.j.units[m] = 0;
-        continue;
       }
       a.j.splits[m] = dw_splits(tiles, a.j.it0[m][runs.n[m]]);
       a.j.units[m] = tiles * a.j.splits[m];
@@ -1036,12 +1084,15 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
     for (int m = 0; m < 2; ++m) {
       if (a.j.splits[m] == 1) continue;
       const int64_t groups = static_cast<int64_t>(N) * (K / 8);
-      dw_parts_kernel<<<static_cast<unsigned>((groups + 255) / 256), 256, 0, st>>>(
-          part, a.j.splits[m], N, K, a.col_tiles, tiles, b.dW + static_cast<size_t>(m) * N * K);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      e = launch_dependent(dw_parts_kernel, dim3(static_cast<unsigned>((groups + 255) / 256)),
+                           dim3(256), 0, st, part, a.j.splits[m], N, K, a.width, a.col_tiles,
+                           tiles, b.dW + static_cast<size_t>(m) * N * K);
+      if (e != cudaSuccess) return e;
       part += static_cast<size_t>(a.j.units[m]) * kTile * kTile;
     }
   }
+  if (db.out != nullptr)
+    return launch_dependent(dz_cols_kernel, dim3((db.cols + 127) / 128), dim3(128), 0, st, db);
   return cudaSuccess;
 }
 

@@ -287,8 +287,7 @@ bool ready() {
 template <bool W_MN>
 cudaError_t launch_rows(const mf_bf16* b, const mf_bf16* W, const TokenRuns& runs,
                         const uint8_t* tok_mod, int32_t T, int32_t K, int32_t N,
-                        const LinearEpilogue& ep, const KernelCtl& ctl, bool dependent,
-                        cudaStream_t st) {
+                        const LinearEpilogue& ep, const KernelCtl& ctl, cudaStream_t st) {
   RowsArgs a;
   a.T = T;
   a.outs = W_MN ? K : N;
@@ -333,7 +332,7 @@ cudaError_t launch_rows(const mf_bf16* b, const mf_bf16* W, const TokenRuns& run
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 2 : 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, linear_rows_kernel<W_MN>, mw, mx, a);
 }
 
@@ -342,7 +341,7 @@ cudaError_t launch_rows(const mf_bf16* b, const mf_bf16* W, const TokenRuns& run
 cudaError_t launch_linear_rows(const mf_bf16* x, const mf_bf16* W, const TokenRuns& runs,
                                const uint8_t* tok_mod, int32_t T, int32_t K, int32_t N,
                                const LinearEpilogue& ep, const KernelCtl& ctl, cudaStream_t st) {
-  return launch_rows<false>(x, W, runs, tok_mod, T, K, N, ep, ctl, false, st);
+  return launch_rows<false>(x, W, runs, tok_mod, T, K, N, ep, ctl, st);
 }
 
 cudaError_t launch_linear_rows_dx(const mf_bf16* dz, const mf_bf16* W, const TokenRuns& runs,
@@ -350,7 +349,7 @@ cudaError_t launch_linear_rows_dx(const mf_bf16* dz, const mf_bf16* W, const Tok
                                   mf_bf16* dx, const KernelCtl& ctl, cudaStream_t st) {
   LinearEpilogue ep{};
   ep.out = dx;
-  return launch_rows<true>(dz, W, runs, tok_mod, T, K, N, ep, ctl, false, st);
+  return launch_rows<true>(dz, W, runs, tok_mod, T, K, N, ep, ctl, st);
 }
 
 }  // namespace mf

@@ -1,6 +1,8 @@
-// pdl.cuh -- programmatic dependent launch: the kernels of one call after its first
-// are launched so that their blocks may come up while the kernel before still runs;
-// each waits for that kernel's end, and for its writes, before it touches memory.
+// pdl.cuh -- programmatic dependent launch: a kernel's blocks may come up while the
+// kernel before it in the stream still runs; each waits for that kernel's end, and for
+// its writes, before it touches memory. What it hides is the launch and the prologue
+// (barriers, tensor memory, tensor maps), which is most of a small call. Behind a
+// kernel that does not release its successors early the launch is an ordinary one.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -11,8 +13,10 @@ namespace mf {
 // (at once in a kernel that was launched the ordinary way).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Lets the next kernel's blocks come up from here on. They wait for this kernel's
-// end all the same, so it can stand anywhere.
+// Lets the next kernel's blocks come up once every block of this one is here. They
+// wait for this kernel's end all the same. It stands behind pdl_wait and behind a
+// kernel's tensor-memory allocation: a block of the next kernel that holds tensor
+// memory must not keep a block of this one from starting.
 __device__ __forceinline__ void pdl_release() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
