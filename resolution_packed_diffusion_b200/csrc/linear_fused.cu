@@ -262,16 +262,51 @@ __device__ __forceinline__ void add_bias32(const float* bias, int left, float (&
     }
 }
 
+// A thread stores runs of its own row, so a warp's store touches 32 rows: with 32
+// bytes a thread it writes whole sectors; with 16 it would write half of each, twice.
+__device__ __forceinline__ void store_sector(void* p, const uint32_t (&r)[8]) {
+  asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ bool sector_aligned(const void* p) {
+  return (reinterpret_cast<uintptr_t>(p) & 31u) == 0;
+}
+
+// Up to 32 columns (`left`, a multiple of 8) in bf16.
 __device__ __forceinline__ void store32(mf_bf16* p, int left, const float (&f)[32]) {
+  const bool wide = sector_aligned(p);
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-    if (q * 8 < left) {
-      const uint4 o = make_uint4(pack_bf16x2(f[8 * q], f[8 * q + 1]),
-                                 pack_bf16x2(f[8 * q + 2], f[8 * q + 3]),
-                                 pack_bf16x2(f[8 * q + 4], f[8 * q + 5]),
-                                 pack_bf16x2(f[8 * q + 6], f[8 * q + 7]));
-      __stcs(reinterpret_cast<uint4*>(p) + q, o);
+  for (int q = 0; q < 2; ++q) {
+    uint32_t r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = pack_bf16x2(f[16 * q + 2 * e], f[16 * q + 2 * e + 1]);
+    if (wide && left >= 16 * (q + 1)) {
+      store_sector(p + 16 * q, r);
+    } else {
+      if (left > 16 * q)
+        __stcs(reinterpret_cast<uint4*>(p + 16 * q), make_uint4(r[0], r[1], r[2], r[3]));
+      if (left > 16 * q + 8)
+        __stcs(reinterpret_cast<uint4*>(p + 16 * q + 8), make_uint4(r[4], r[5], r[6], r[7]));
     }
+  }
+}
+
+// Up to 32 codes.
+__device__ __forceinline__ void store32_codes(int8_t* p, int left, const float (&f)[32], float inv,
+                                              uint32_t mask) {
+  uint32_t r[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    r[e] = act8_code4(f2_pack(f[4 * e], f[4 * e + 1]), f2_pack(f[4 * e + 2], f[4 * e + 3]), inv, mask);
+  if (left >= 32 && sector_aligned(p)) {
+    store_sector(p, r);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (left > 8 * q)
+        __stcs(reinterpret_cast<uint2*>(p) + q, make_uint2(r[2 * q], r[2 * q + 1]));
+  }
 }
 
 // The forward's epilogue on columns [cc0, cc1) of one row of a tile (a block of
@@ -309,16 +344,7 @@ __device__ __forceinline__ void forward_row(const Args<kFwd>& a, uint32_t taddr,
     float f[32];
     acc_load32(taddr + cc, f);
     if (bias != nullptr) add_bias32(bias + c0, left, f);
-    if (ep.z8 != nullptr && keep) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q * 8 < left)
-          __stcs(reinterpret_cast<uint2*>(ep.z8 + rowoff + c0) + q,
-                 make_uint2(act8_code4(f2_pack(f[8 * q], f[8 * q + 1]),
-                                       f2_pack(f[8 * q + 2], f[8 * q + 3]), inv, mask),
-                            act8_code4(f2_pack(f[8 * q + 4], f[8 * q + 5]),
-                                       f2_pack(f[8 * q + 6], f[8 * q + 7]), inv, mask)));
-    }
+    if (ep.z8 != nullptr && keep) store32_codes(ep.z8 + rowoff + c0, left, f, inv, mask);
     if (ep.z != nullptr && keep) store32(ep.z + rowoff + c0, left, f);
     if (ep.act == MF_ACT_GELU) act32<MF_ACT_GELU>(f);
     if (ep.act == MF_ACT_SILU) act32<MF_ACT_SILU>(f);
@@ -573,9 +599,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             for (int e = 0; e < 32; ++e) f[e] = 0.f;
           if (part != nullptr) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              *(reinterpret_cast<float4*>(part + cc) + q) =
-                  make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t r[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) r[e] = __float_as_uint(f[8 * q + e]);
+              store_sector(part + cc + 8 * q, r);
+            }
           } else if (keep) {
             store32(out + cc, end - cc, f);
           }
