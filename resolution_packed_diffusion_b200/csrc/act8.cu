@@ -38,25 +38,24 @@ __device__ __forceinline__ uint32_t absmax_bits(const uint4& u) {
   return max(m & 0xFFFFu, m >> 16);
 }
 
-// items = T * nb blocks in row order; item i is block i % nb of row i / nb.
 __global__ void __launch_bounds__(kThreads) act8_quantize_kernel(const mf_bf16* __restrict__ x,
-                                                                 int64_t items, int nb, int C,
+                                                                 const Act8Rows rows,
                                                                  int8_t* __restrict__ q,
                                                                  float* __restrict__ scale) {
   pdl_wait();
   pdl_release();
   const int lane = threadIdx.x % kLanes;
-  const int64_t base = blockIdx.x * static_cast<int64_t>(kPerCta * kUnroll) + threadIdx.x / kLanes;
+  const uint32_t base = blockIdx.x * (kPerCta * kUnroll) + threadIdx.x / kLanes;
   uint4 v[kUnroll];
   int64_t off[kUnroll];
   bool in[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const int64_t item = base + u * kPerCta;
-    const int64_t row = item / nb;
-    const int c = static_cast<int>(item - row * nb) * kAct8Block + lane * 8;
-    in[u] = item < items && c < C;
-    off[u] = row * C + c;
+    const uint32_t item = base + u * kPerCta;
+    const uint32_t row = rows.nb.div(item);
+    const int c = static_cast<int>(item - row * rows.nb.d) * kAct8Block + lane * 8;
+    in[u] = item < rows.items && c < rows.C;
+    off[u] = static_cast<int64_t>(row) * rows.C + c;
     v[u] = in[u] ? __ldcs(reinterpret_cast<const uint4*>(x + off[u])) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
@@ -66,51 +65,58 @@ __global__ void __launch_bounds__(kThreads) act8_quantize_kernel(const mf_bf16* 
     for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     float s, inv;
     uint64_t f[4];
-    act8_scale(__uint_as_float(m << 16), s, inv);
+    act8_scale_pairwise(__uint_as_float(m << 16), lane & 1, s, inv);
     const uint32_t mask = inv == 0.f ? 0u : 0xFFFFFFFFu;
     bf16x8_f2(v[u], f);
     if (in[u])
       __stcs(reinterpret_cast<uint2*>(q + off[u]),
              make_uint2(act8_code4(f[0], f[1], inv, mask), act8_code4(f[2], f[3], inv, mask)));
-    const int64_t item = base + u * kPerCta;
-    if (lane == 0 && item < items) scale[item] = s;
+    const uint32_t item = base + u * kPerCta;
+    if (lane == 0 && item < rows.items) scale[item] = s;
   }
 }
 
 template <int ACT>
 __global__ void __launch_bounds__(kThreads) act8_dequantize_kernel(const int8_t* __restrict__ q,
                                                                    const float* __restrict__ scale,
-                                                                   int64_t items, int nb, int C,
+                                                                   const Act8Rows rows,
                                                                    mf_bf16* __restrict__ y) {
   pdl_wait();
   pdl_release();
-  act8_decode<ACT>(q, scale, items, nb, C, y, blockIdx.x);
+  act8_decode<ACT>(q, scale, rows, y, blockIdx.x);
 }
 
 }  // namespace
 
-// T <= 2^24 and nb <= 2^13 keep the grid within 2^31 (one CTA per 64 blocks).
 cudaError_t launch_act8_quantize(const mf_bf16* x, int32_t T, int32_t C, int8_t* q, float* scale,
                                  cudaStream_t st) {
-  const int nb = act8_blocks(C);
-  const int64_t items = static_cast<int64_t>(T) * nb;
-  return launch_dependent(act8_quantize_kernel, dim3(act8_decode_blocks(items)), dim3(kThreads), 0,
-                          st, x, items, nb, C, q, scale);
+  for (int32_t t = 0, n; t < T; t += n) {
+    n = T - t < act8_rows_max(C) ? T - t : act8_rows_max(C);
+    const Act8Rows rows = act8_rows(n, C);
+    const cudaError_t e = launch_dependent(
+        act8_quantize_kernel, dim3(act8_decode_blocks(rows.items)), dim3(kThreads), 0, st,
+        x + static_cast<size_t>(t) * C, rows, q + static_cast<size_t>(t) * C,
+        scale + static_cast<size_t>(t) * act8_blocks(C));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_act8_dequantize(const int8_t* q, const float* scale, int32_t T, int32_t C,
                                    int32_t act, mf_bf16* y, cudaStream_t st) {
-  const int nb = act8_blocks(C);
-  const int64_t items = static_cast<int64_t>(T) * nb;
-  const dim3 grid(act8_decode_blocks(items)), block(kThreads);
-  if (act == MF_ACT_GELU)
-    return launch_dependent(act8_dequantize_kernel<MF_ACT_GELU>, grid, block, 0, st, q, scale,
-                            items, nb, C, y);
-  if (act == MF_ACT_SILU)
-    return launch_dependent(act8_dequantize_kernel<MF_ACT_SILU>, grid, block, 0, st, q, scale,
-                            items, nb, C, y);
-  return launch_dependent(act8_dequantize_kernel<MF_ACT_NONE>, grid, block, 0, st, q, scale, items,
-                          nb, C, y);
+  auto kernel = act == MF_ACT_GELU   ? act8_dequantize_kernel<MF_ACT_GELU>
+                : act == MF_ACT_SILU ? act8_dequantize_kernel<MF_ACT_SILU>
+                                     : act8_dequantize_kernel<MF_ACT_NONE>;
+  for (int32_t t = 0, n; t < T; t += n) {
+    n = T - t < act8_rows_max(C) ? T - t : act8_rows_max(C);
+    const Act8Rows rows = act8_rows(n, C);
+    const cudaError_t e = launch_dependent(
+        kernel, dim3(act8_decode_blocks(rows.items)), dim3(kThreads), 0, st,
+        q + static_cast<size_t>(t) * C, scale + static_cast<size_t>(t) * act8_blocks(C), rows,
+        y + static_cast<size_t>(t) * C);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace mf

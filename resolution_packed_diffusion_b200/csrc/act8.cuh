@@ -78,6 +78,18 @@ __device__ __forceinline__ void act8_scale(float amax, float& s, float& inv) {
   inv = bad || zero ? 0.f : __fdiv_rn(127.f, amax);
 }
 
+// The same by a whole warp whose even and odd lanes share a block: one division a
+// lane, exchanged.
+__device__ __forceinline__ void act8_scale_pairwise(float amax, bool odd, float& s, float& inv) {
+  const bool bad = !(amax <= 3.402823466e38f);
+  const bool zero = amax < 7.888609052e-31f;
+  const float a = bad || zero ? 1.f : amax;
+  const float mine = __fdiv_rn(odd ? 127.f : a, odd ? a : 127.f);
+  const float other = __shfl_xor_sync(0xffffffffu, mine, 1);
+  s = bad ? __uint_as_float(0x7FC00000u) : (zero ? 0.f : (odd ? other : mine));
+  inv = bad || zero ? 0.f : (odd ? mine : other);
+}
+
 // Four codes of (a.lo, a.hi, b.lo, b.hi) under the reciprocal step: round to nearest
 // even of the rounded product, so |code| <= 127 (1.5 * 2^23 added, the integer is
 // in the low bits of the sum). The products are scalar: the compiler contracts a
@@ -179,29 +191,56 @@ constexpr int kAct8Unroll = 4;
 constexpr int kAct8Lanes = kAct8Block / 8;
 constexpr int kAct8PerCta = kAct8Threads / kAct8Lanes;  // blocks a CTA takes per step
 
-inline unsigned act8_decode_blocks(int64_t items) {
-  return static_cast<unsigned>((items + kAct8PerCta * kAct8Unroll - 1) / (kAct8PerCta * kAct8Unroll));
+inline unsigned act8_decode_blocks(uint32_t items) {
+  return (items + kAct8PerCta * kAct8Unroll - 1) / (kAct8PerCta * kAct8Unroll);
+}
+
+// n / d for n < 2^31 by one high product (Granlund and Montgomery's method): with
+// 2^shift >= d, mul = floor(2^32 (2^shift - d) / d) + 1, the quotient is
+// (mulhi(mul, n) + n) >> shift.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(mul, n) + n) >> shift; }
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f = {d, 0, 0};
+  while ((1u << f.shift) < d) ++f.shift;
+  f.mul = static_cast<uint32_t>(((uint64_t{1} << 32) * ((uint64_t{1} << f.shift) - d)) / d + 1);
+  return f;
+}
+
+// Where block `item` of the checkpoint lies: its row and first channel.
+struct Act8Rows {
+  FastDiv nb;      // blocks of a row
+  int32_t C;
+  uint32_t items;  // rows x blocks, below 2^31
+};
+// Rows of one launch, so that its items stay below 2^31.
+inline int32_t act8_rows_max(int32_t C) { return 0x7FFFFFFF / act8_blocks(C); }
+inline Act8Rows act8_rows(int32_t T, int32_t C) {
+  const uint32_t nb = act8_blocks(C);
+  return Act8Rows{fast_div(nb), C, static_cast<uint32_t>(T) * nb};
 }
 
 template <int ACT>
 __device__ __forceinline__ void act8_decode(const int8_t* __restrict__ q,
-                                            const float* __restrict__ scale, int64_t items, int nb,
-                                            int C, mf_bf16* __restrict__ y, int64_t block) {
+                                            const float* __restrict__ scale, const Act8Rows& rows,
+                                            mf_bf16* __restrict__ y, uint32_t block) {
   const int lane = threadIdx.x % kAct8Lanes;
-  const int64_t base = block * (kAct8PerCta * kAct8Unroll) + threadIdx.x / kAct8Lanes;
+  const uint32_t base = block * (kAct8PerCta * kAct8Unroll) + threadIdx.x / kAct8Lanes;
   uint2 v[kAct8Unroll];
   float s[kAct8Unroll];
   int64_t off[kAct8Unroll];
   bool in[kAct8Unroll];
 #pragma unroll
   for (int u = 0; u < kAct8Unroll; ++u) {
-    const int64_t item = base + u * kAct8PerCta;
-    const int64_t row = item / nb;
-    const int c = static_cast<int>(item - row * nb) * kAct8Block + lane * 8;
-    in[u] = item < items && c < C;
-    off[u] = row * C + c;
+    const uint32_t item = base + u * kAct8PerCta;
+    const uint32_t row = rows.nb.div(item);
+    const int c = static_cast<int>(item - row * rows.nb.d) * kAct8Block + lane * 8;
+    in[u] = item < rows.items && c < rows.C;
+    off[u] = static_cast<int64_t>(row) * rows.C + c;
     v[u] = in[u] ? __ldcs(reinterpret_cast<const uint2*>(q + off[u])) : make_uint2(0, 0);
-    s[u] = item < items ? __ldg(scale + item) : 0.f;
+    s[u] = item < rows.items ? __ldg(scale + item) : 0.f;
   }
 #pragma unroll
   for (int u = 0; u < kAct8Unroll; ++u) {

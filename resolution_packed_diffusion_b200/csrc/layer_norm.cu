@@ -338,12 +338,13 @@ constexpr int kBwdRows = 2;  // rows per group and step: an even number, so that
                              // step's 8-bit codes start on a 16-byte boundary
 constexpr int kMaxStages = 4;
 
-// A thread owns CH chunks of eight channels, a.lanes chunks apart. part:
+// A thread owns CH chunks of eight channels, a.lanes chunks apart; FULL: all of them
+// exist (hid is 8 CH lanes), so nothing is guarded by the width. part:
 // [grid][2 modalities][2 (dgamma, dbeta)][hid], or dgamma and dbeta themselves when
 // the grid is one CTA (part NULL). Dynamic shared memory: the stages, then, with
 // more than one group, [groups][2][2][hid] fp32. One group adds into its place in
 // memory directly: each column has one owner.
-template <int SUB, int CH, int THREADS, int PER_SM, bool X8>
+template <int SUB, int CH, int THREADS, int PER_SM, bool FULL, bool X8>
 __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
     const mf_bf16* __restrict__ dy, const mf_bf16* __restrict__ x, const Act8 x8,
     const float* __restrict__ gamma, const float2* __restrict__ stats, const mf_bf16* resid,
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
   const int warps = a.lanes / 32, lane = threadIdx.x & 31;
   bool on[CH];
 #pragma unroll
-  for (int j = 0; j < CH; ++j) on[j] = (gl + j * a.lanes) * 8 < a.hid;
+  for (int j = 0; j < CH; ++j) on[j] = FULL || (gl + j * a.lanes) * 8 < a.hid;
   const float inv_n = 1.f / static_cast<float>(a.hid);
   const int nb = (a.hid + kAct8Block - 1) / kAct8Block;
   int r0, r1;
@@ -507,18 +508,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
       for (int e = 0; e < 4; ++e) h[e] = f2_fma(h[e], r2, m2);
     };
     float sums[2 * R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      sums[2 * i] = sums[2 * i + 1] = 0.f;
-      if (mod[i] < 0) continue;
-      if (mod[i] != cm) {
-        flush();
-        cm = mod[i];
-#pragma unroll
-        for (int j = 0; j < CH; ++j)
-          if (on[j])
-            load8_f2(gamma + static_cast<size_t>(cm) * a.hid + (gl + j * a.lanes) * 8, gam[j]);
-      }
+    auto accumulate = [&](int i) {
       uint64_t s1 = 0, s2 = 0;
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
@@ -539,6 +529,29 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
       sums[2 * i] = lo + hi;
       f2_unpack(s2, lo, hi);
       sums[2 * i + 1] = lo + hi;
+    };
+    // nearly every step is of one modality throughout: one test, no more
+    bool usual = cm >= 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) usual = usual && mod[i] == cm;
+    if (usual) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) accumulate(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        sums[2 * i] = sums[2 * i + 1] = 0.f;
+        if (mod[i] < 0) continue;
+        if (mod[i] != cm) {
+          flush();
+          cm = mod[i];
+#pragma unroll
+          for (int j = 0; j < CH; ++j)
+            if (on[j])
+              load8_f2(gamma + static_cast<size_t>(cm) * a.hid + (gl + j * a.lanes) * 8, gam[j]);
+        }
+        accumulate(i);
+      }
     }
     // The four sums over a group's lanes. Lane l ends with sum l mod 4: two rounds
     // that halve the sums a lane holds, then plain ones (6 shuffles in place of 20).
@@ -589,9 +602,14 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
         *reinterpret_cast<uint4*>(out + static_cast<size_t>(i) * a.hid + j * chunk) = f2_bf16x8(o);
       }
     };
+    if (usual) {
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (mod[i] >= 0) finish(i, mod[i] != cm);
+      for (int i = 0; i < R; ++i) finish(i, false);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (mod[i] >= 0) finish(i, mod[i] != cm);
+    }
     prev = at;
     if (++at == sg.stages) {
       at = 0;
@@ -693,7 +711,7 @@ RowShape bwd_row_shape(int32_t hid) {
 
 // CTAs per SM: several, so that one computes while another waits at its barrier; one
 // above 256 threads, whose registers leave no more room.
-int bwd_per_sm(const RowShape& s) { return s.threads > 256 ? 1 : s.groups > 1 || s.threads > 128 ? 2 : 3; }
+int bwd_per_sm(const RowShape& s) { return s.threads > 256 ? 1 : 2; }
 
 BwdStage bwd_stage(const RowShape& s, int32_t hid, bool x8, bool resid) {
   auto round128 = [](int v) { return (v + 127) / 128 * 128; };
@@ -718,11 +736,11 @@ int bwd_grid(const RowShape& s, int32_t T) {
   return by_steps < sms ? sms : by_steps < cap ? by_steps : cap;
 }
 
-template <int SUB, int CH, int THREADS, int PER_SM, bool X8>
+template <int SUB, int CH, int THREADS, int PER_SM, bool FULL, bool X8>
 cudaError_t bwd_shape(const mf_bf16* dy, const mf_bf16* x, const Act8& x8, const float* gamma,
                       const float* stats, const mf_bf16* resid, const LnArgs& a, const RowShape& s,
                       mf_bf16* dx, float* dgamma, float* dbeta, float* part, cudaStream_t st) {
-  auto kernel = layer_norm_bwd_kernel<SUB, CH, THREADS, PER_SM, X8>;
+  auto kernel = layer_norm_bwd_kernel<SUB, CH, THREADS, PER_SM, FULL, X8>;
   const BwdStage g = bwd_stage(s, a.hid, X8, resid != nullptr);
   const int smem = g.stages * g.bytes() + (s.groups > 1 ? s.groups * 16 * a.hid : 0);
   const cudaError_t ae =
@@ -768,18 +786,20 @@ cudaError_t launch_layer_norm_bwd(const mf_bf16* dy, const mf_bf16* x, const Act
   const RowShape s = bwd_row_shape(hid);
   const LnArgs a{tok_mod, T, hid, s.lanes, s.groups, ctl};
   float* part = reinterpret_cast<float*>(ws);
-#define MF_LN_BWD(SUB, CH, THREADS, PER_SM)                                                  \
-  (x8.q != nullptr                                                                           \
-       ? bwd_shape<SUB, CH, THREADS, PER_SM, true>(dy, x, x8, gamma, stats, resid, a, s, dx, \
-                                                   dgamma, dbeta, part, st)                  \
-       : bwd_shape<SUB, CH, THREADS, PER_SM, false>(dy, x, x8, gamma, stats, resid, a, s, dx, \
-                                                    dgamma, dbeta, part, st))
-  if (s.lanes == 8) return MF_LN_BWD(8, 1, 256, 2);
-  if (s.lanes == 16) return MF_LN_BWD(16, 1, 256, 2);
-  if (hid <= 2048) return MF_LN_BWD(32, 1, 256, 2);
-  if (hid <= 3072) return MF_LN_BWD(32, 2, 192, 2);
-  if (hid <= 4096) return MF_LN_BWD(32, 2, 256, 2);
-  return MF_LN_BWD(32, 2, 512, 1);
+#define MF_LN_BWD(SUB, CH, THREADS, PER_SM, FULL)                                              \
+  (x8.q != nullptr                                                                             \
+       ? bwd_shape<SUB, CH, THREADS, PER_SM, FULL, true>(dy, x, x8, gamma, stats, resid, a, s, \
+                                                         dx, dgamma, dbeta, part, st)          \
+       : bwd_shape<SUB, CH, THREADS, PER_SM, FULL, false>(dy, x, x8, gamma, stats, resid, a, s, \
+                                                          dx, dgamma, dbeta, part, st))
+  if (s.lanes == 8) return MF_LN_BWD(8, 1, 256, 2, false);
+  if (s.lanes == 16) return MF_LN_BWD(16, 1, 256, 2, false);
+  if (hid <= 2048)
+    return hid == 8 * s.lanes ? MF_LN_BWD(32, 1, 256, 2, true) : MF_LN_BWD(32, 1, 256, 2, false);
+  const bool full = hid == 16 * s.lanes;
+  if (hid <= 3072) return full ? MF_LN_BWD(32, 2, 192, 2, true) : MF_LN_BWD(32, 2, 192, 2, false);
+  if (hid <= 4096) return full ? MF_LN_BWD(32, 2, 256, 2, true) : MF_LN_BWD(32, 2, 256, 2, false);
+  return full ? MF_LN_BWD(32, 2, 512, 1, true) : MF_LN_BWD(32, 2, 512, 1, false);
 #undef MF_LN_BWD
 }
 

@@ -703,8 +703,7 @@ int dz_rows(int32_t T) { return T <= 2048 ? 32 : T <= 8192 ? 64 : 128; }
 
 struct Decode {
   Act8 x8;
-  int64_t items;   // blocks of 128 channels; 0: nothing to decode
-  int32_t nb, C;
+  Act8Rows rows;  // no items: nothing to decode
   mf_bf16* y;
 };
 
@@ -719,8 +718,7 @@ __global__ void __launch_bounds__(256) dz_kernel(const mf_bf16* __restrict__ dou
   pdl_wait();
   pdl_release();
   if (static_cast<int>(blockIdx.x) >= dz_blocks) {
-    act8_decode<MF_ACT_NONE>(dec.x8.q, dec.x8.scale, dec.items, dec.nb, dec.C, dec.y,
-                             blockIdx.x - dz_blocks);
+    act8_decode<MF_ACT_NONE>(dec.x8.q, dec.x8.scale, dec.rows, dec.y, blockIdx.x - dz_blocks);
     return;
   }
   const int chunk = blockIdx.x / col_blocks, cb = blockIdx.x - chunk * col_blocks;
@@ -1043,10 +1041,10 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
   // as the product.
   Decode dec = {};
   if (b.dW != nullptr && b.x == nullptr)
-    dec = Decode{b.x8, static_cast<int64_t>(T) * act8_blocks(K), act8_blocks(K), K, x_ws};
+    dec = Decode{b.x8, act8_rows(T, K), x_ws};  // T blocks <= 2^17 2^13: below 2^31
   const int col_blocks = (N + 255) / 256;
   const int dz_blocks = b.act != MF_ACT_NONE || b.db != nullptr ? chunks * col_blocks : 0;
-  const unsigned blocks = dz_blocks + act8_decode_blocks(dec.items);
+  const unsigned blocks = dz_blocks + act8_decode_blocks(dec.rows.items);
   if (blocks > 0) {
     float* p = b.db == nullptr ? nullptr : chunks > 1 ? part : b.db;
 #define MF_DZ(ACT, Z8)                                                                           \
