@@ -727,12 +727,12 @@ BwdStage bwd_stage(const RowShape& s, int32_t hid, bool x8, bool resid) {
   return g;
 }
 
-// One CTA per step up to one per SM, then whole multiples of eight steps: each CTA
-// leaves column sums for the second kernel to add.
+// One CTA per step up to one per SM, then one per four steps: each CTA leaves column
+// sums for the second kernel to add.
 int bwd_grid(const RowShape& s, int32_t T) {
   const int steps = (T + s.groups * kBwdRows - 1) / (s.groups * kBwdRows), sms = ln_sms();
   if (steps <= sms) return steps;
-  const int by_steps = steps / 8, cap = sms * bwd_per_sm(s);
+  const int by_steps = steps / 4, cap = sms * bwd_per_sm(s);
   return by_steps < sms ? sms : by_steps < cap ? by_steps : cap;
 }
 

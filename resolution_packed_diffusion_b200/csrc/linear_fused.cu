@@ -80,7 +80,8 @@ constexpr int kDrain = kAccEmpty + 2;
 constexpr int kNumBars = kDrain + 1;
 constexpr int kOffBar = kStages * kStageBytes;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;  // TMEM address, abort flag
-constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+constexpr int kOffBias = kOffMisc + 16;           // the tile's bias: 256 floats
+constexpr int kSmemBytes = kOffBias + kTile * 4 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA");
 
 // One (row block, modality) job per entry for the forward and dx.
@@ -157,6 +158,8 @@ __device__ __forceinline__ void load_w(void* dst, const CUtensorMap* map, uint32
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
       : "memory");
 }
+
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const KernelCtl& ctl,
                                           volatile int* abort_flag) {
@@ -250,17 +253,36 @@ __device__ __forceinline__ void act32(float (&v)[32]) {
   }
 }
 
-__device__ __forceinline__ void add_bias32(const float* bias, int left, float (&f)[32]) {
+// 32 columns' bias, the same for every row: broadcast reads of shared memory.
+__device__ __forceinline__ void add_bias32(const float* bias, float (&f)[32]) {
 #pragma unroll
-  for (int q = 0; q < 8; ++q)
-    if (q * 4 < left) {  // the width is a multiple of 8
-      const float4 b = __ldg(reinterpret_cast<const float4*>(bias) + q);
-      f[4 * q] += b.x;
-      f[4 * q + 1] += b.y;
-      f[4 * q + 2] += b.z;
-      f[4 * q + 3] += b.w;
-    }
+  for (int q = 0; q < 8; ++q) {
+    const float4 b = *(reinterpret_cast<const float4*>(bias) + q);
+    f[4 * q] += b.x;
+    f[4 * q + 1] += b.y;
+    f[4 * q + 2] += b.z;
+    f[4 * q + 3] += b.w;
+  }
 }
+
+// 32 columns of a residual row, as far as they exist.
+struct Resid32 {
+  uint4 v[4];
+  __device__ __forceinline__ void load(const mf_bf16* p, int left) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      v[q] = q * 8 < left ? *(reinterpret_cast<const uint4*>(p) + q) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void add(float (&f)[32]) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float r[8];
+      bf16x8_unpack(v[q], r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[8 * q + e] += r[e];
+    }
+  }
+};
 
 // A thread stores runs of its own row, so a warp's store touches 32 rows: with 32
 // bytes a thread it writes whole sectors; with 16 it would write half of each, twice.
@@ -312,13 +334,14 @@ __device__ __forceinline__ void store32_codes(int8_t* p, int left, const float (
 // The forward's epilogue on columns [cc0, cc1) of one row of a tile (a block of
 // scales at most): bias, the kept pre-activation, activation, residual. With an
 // 8-bit checkpoint the row's values of the block are read twice from TMEM, once for
-// their largest magnitude; z itself never reaches memory.
-__device__ __forceinline__ void forward_row(const Args<kFwd>& a, uint32_t taddr, int t, int m,
-                                            bool keep, int n0, int cc0, int cc1) {
+// their largest magnitude; z itself never reaches memory. bias: the tile's, in shared
+// memory, or NULL; res: the residual's first 32 columns, asked for before the
+// accumulator was waited for (each next 32 are asked for one step ahead).
+__device__ __forceinline__ void forward_row(const Args<kFwd>& a, uint32_t taddr, int t, bool keep,
+                                            int n0, int cc0, int cc1, const float* bias,
+                                            Resid32& res) {
   const LinearEpilogue& ep = a.ep;
   const size_t rowoff = static_cast<size_t>(t) * a.N;
-  const float* bias = ep.bias == nullptr ? nullptr : ep.bias + static_cast<size_t>(m) * a.N;
-  if (n0 + cc1 > a.N) cc1 = a.N - n0;
   float s = 0.f, inv = 0.f;
   uint32_t mask = 0;
   if (ep.z8 != nullptr && cc0 < cc1) {
@@ -327,7 +350,7 @@ __device__ __forceinline__ void forward_row(const Args<kFwd>& a, uint32_t taddr,
     for (int cc = cc0; cc < cc1; cc += 32) {
       float f[32];
       acc_load32(taddr + cc, f);
-      if (bias != nullptr) add_bias32(bias + n0 + cc, cc1 - cc, f);
+      if (bias != nullptr) add_bias32(bias + cc, f);
 #pragma unroll
       for (int e = 0; e < 32; ++e)
         if (e < cc1 - cc) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
@@ -342,25 +365,19 @@ __device__ __forceinline__ void forward_row(const Args<kFwd>& a, uint32_t taddr,
   for (int cc = cc0; cc < cc1; cc += 32) {
     const int c0 = n0 + cc, left = cc1 - cc;
     float f[32];
+    Resid32 next;
+    if (ep.resid != nullptr && keep) next.load(ep.resid + rowoff + c0 + 32, left - 32);
     acc_load32(taddr + cc, f);
-    if (bias != nullptr) add_bias32(bias + c0, left, f);
+    if (bias != nullptr) add_bias32(bias + cc, f);
     if (ep.z8 != nullptr && keep) store32_codes(ep.z8 + rowoff + c0, left, f, inv, mask);
     if (ep.z != nullptr && keep) store32(ep.z + rowoff + c0, left, f);
     if (ep.act == MF_ACT_GELU) act32<MF_ACT_GELU>(f);
     if (ep.act == MF_ACT_SILU) act32<MF_ACT_SILU>(f);
     if (keep) {
-      if (ep.resid != nullptr) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (q * 8 < left) {
-            float r[8];
-            bf16x8_unpack(*(reinterpret_cast<const uint4*>(ep.resid + rowoff + c0) + q), r);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[8 * q + e] += r[e];
-          }
-      }
+      if (ep.resid != nullptr) res.add(f);
       store32(ep.out + rowoff + c0, left, f);
     }
+    res = next;
   }
 }
 
@@ -554,18 +571,37 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const int cc0 = warp >= 8 ? kTile / 2 : 0;
     const int cc1 = warp >= 8 ? args.width : min(kTile / 2, args.width);
     uint32_t ul = 0;
+    bool stop = false;  // a wait ran out: the forward's warps still meet at their barrier
     for (int u = unit0; u < units; u += stride, ++ul) {
       const uint32_t acc = ul & 1;
-      if (!warp_wait(&bars[kAccFull + acc], (ul >> 1) & 1, args.ctl, abort_flag)) break;
-      tc_fence_after();
       const uint32_t taddr = tmem + lane_base + acc * kTile;
       if constexpr (MODE == kFwd) {
         int blk = 0, m = 0, ct = 0;
         row_job(u, blk, m, ct);
-        const int t = blk * kTile + rank * kHalf + row;
+        const int t = blk * kTile + rank * kHalf + row, n0 = ct * args.width;
         const bool keep = t < args.T && __ldg(args.tok_mod + t) == m;
-        forward_row(args, taddr, t, m, keep, ct * args.width, cc0, cc1);
+        const int end = min(cc1, args.N - n0);
+        float* bias = reinterpret_cast<float*>(smem + kOffBias);
+        Resid32 res;
+        if (args.ep.resid != nullptr && keep && cc0 < end)
+          res.load(args.ep.resid + static_cast<size_t>(t) * args.N + n0 + cc0, end - cc0);
+        if (args.ep.bias != nullptr) {
+          const int c = static_cast<int>(threadIdx.x) - 4 * 32;
+          const float v = n0 + c < args.N
+                              ? __ldg(args.ep.bias + static_cast<size_t>(m) * args.N + n0 + c)
+                              : 0.f;
+          epilogue_sync();  // every warp is done with the tile before
+          bias[c] = v;
+          epilogue_sync();
+        }
+        if (!warp_wait(&bars[kAccFull + acc], (ul >> 1) & 1, args.ctl, abort_flag)) stop = true;
+        tc_fence_after();
+        if (!stop)
+          forward_row(args, taddr, t, keep, n0, cc0, end, args.ep.bias != nullptr ? bias : nullptr,
+                      res);
       } else {
+        if (!warp_wait(&bars[kAccFull + acc], (ul >> 1) & 1, args.ctl, abort_flag)) break;
+        tc_fence_after();
         int k0;
         bool keep;
         mf_bf16* out;
