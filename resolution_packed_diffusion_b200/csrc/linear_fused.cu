@@ -120,7 +120,7 @@ struct Args {
   typename JobsOf<MODE>::type j;
   int32_t T, K, N;
   int32_t n_steps;         // steps of the inner dimension (forward, dx)
-  int32_t width;           // columns of a tile: 256, 128 or 64
+  int32_t width;           // columns of a tile: a multiple of 16, at most 256
   int32_t col_tiles;       // column tiles of the output
   int32_t nb;              // column tiles per block of the traversal
   const uint8_t* tok_mod;
@@ -938,14 +938,32 @@ void row_jobs(const TokenRuns& runs, int32_t T, GemmJobs* jobs) {
 
 // Width of the column tiles: 256, or 128 or 64 while all tiles then still fit one
 // round over the pairs of SMs (short packs, small layers: the epilogue, which no next
-// tile's MMAs hide there, shrinks with the width). Filling the last of several rounds
-// by other widths did not pay: at 8464 x 3072 x 12288 width 240 runs 22.5 rounds'
-// worth instead of 23 and takes 502 us instead of 483, the copies of A growing and
-// the halves leaving the 64-column atoms.
+// tile's MMAs hide there, shrinks with the width).
 int tile_width(int rows, int cols, int pairs, int least) {
   int w = kTile;
   while (w / 2 >= least && rows * ((cols + w / 2 - 1) / (w / 2)) <= pairs) w /= 2;
   return w;
+}
+
+// The forward's, in two or three rounds: the width whose rounds cost least, a round
+// as much as its width and 200 columns more (1000 -> 2056 over 2751 tokens: 208
+// columns, 30.2 us against 32.9). Beyond that 256 is best whatever the last round
+// holds (8464 x 3072 x 12288: 240 columns would be 22.5 rounds' worth in place of 23
+// and take 502 us in place of 483), and dx, whose B operand comes in 64-column boxes,
+// gains nothing from other widths (33.8 us at 240 against 30.9, 4096 -> 1024 over 2464).
+int forward_width(int rows, int cols, int pairs, bool blocks) {
+  const int w = tile_width(rows, cols, pairs, blocks ? kAct8Block : 64);
+  if (w < kTile || blocks || pairs <= 0) return w;
+  int best = w, cost = 0;
+  for (int v = kTile; v >= 128; v -= 16) {
+    const int rounds = (rows * ((cols + v - 1) / v) + pairs - 1) / pairs;
+    if (v == kTile && rounds > 3) return kTile;
+    if (v == kTile || rounds * (v + 200) < cost) {
+      best = v;
+      cost = rounds * (v + 200);
+    }
+  }
+  return best;
 }
 
 template <int MODE>
@@ -1036,8 +1054,7 @@ cudaError_t launch_linear_fused(const mf_bf16* x, const mf_bf16* W, const TokenR
   if (few_rows(T)) return launch_linear_rows(x, W, runs, tok_mod, T, K, N, ep, ctl, st);
   static thread_local Args<kFwd> a;
   row_jobs(runs, T, &a.j.jobs);
-  fill(a, T, K, N, N, tile_width(a.j.jobs.n, N, max_clusters<kFwd>(),
-                                    ep.z8 != nullptr ? kAct8Block : 64), ctl);
+  fill(a, T, K, N, N, forward_width(a.j.jobs.n, N, max_clusters<kFwd>(), ep.z8 != nullptr), ctl);
   CUtensorMap ma, mb;
   if (!linear_map(&ma, x, K, T, 0, kHalf) || !linear_map(&mb, W, K, N, 2, a.width / 2))
     return cudaErrorInvalidValue;
