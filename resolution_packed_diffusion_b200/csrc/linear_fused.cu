@@ -12,9 +12,10 @@
 //
 // One kernel template carries the three products (clusters of two CTAs on two
 // SMs, cta_group::2: 256 x 256 output tiles as M = 256, N = 256 MMAs with fp32
-// accumulators in TMEM, 64 of the inner dimension per stage). Nothing is
-// transposed in memory: the operands are read as they lie, and the tensor core's
-// descriptors say which way they run.
+// accumulators in TMEM, 64 of the inner dimension per stage); the backward's two run
+// in one launch, their tiles in one queue, the longest first, so that neither leaves
+// SMs idle at its end. Nothing is transposed in memory: the operands are read as they
+// lie, and the tensor core's descriptors say which way they run.
 //   forward  A = x (inner dimension contiguous), B = W (contiguous)
 //   dx       A = dz (contiguous),                B = W (inner dimension strided)
 //   dW       A = dz, B = x (both strided: the inner dimension is the tokens)
@@ -31,8 +32,8 @@
 // step, against 0.45 us for its copies and MMAs.
 //   warp 0      TMA producer (one lane)
 //   warp 1      tcgen05 issuer (one lane of the leader CTA)
-//   warp 2      dW only: zeroes the rows past a run
-//   warp 3      dx or dW: adds the partial sums of db that dz_kernel left
+//   warp 2      backward: zeroes the rows past a run
+//   warp 3      backward: adds the partial sums of db that dz_kernel left
 //   warps 4..11 epilogue, from the accumulator that the MMAs have left for the other
 //               one of the two: one output row and half of the columns per thread
 // Every wait is bounded.
@@ -54,7 +55,7 @@ namespace mf {
 
 namespace {
 
-constexpr int kFwd = 0, kDx = 1, kDw = 2;
+constexpr int kFwd = 0, kBwd = 1;
 constexpr int kHalf = 128;   // output rows, and B columns, of one CTA of the pair
 constexpr int kTile = 256;   // output tile: rows, and columns at most
 constexpr int kStepK = 64;   // inner dimension per stage: one 128-byte swizzle atom
@@ -84,21 +85,6 @@ constexpr int kOffBias = kOffMisc + 16;           // the tile's bias: 256 floats
 constexpr int kSmemBytes = kOffBias + kTile * 4 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget of one CTA");
 
-// One (row block, modality) job per entry for the forward and dx.
-struct RowJobs {
-  GemmJobs jobs;
-};
-// The modalities' runs for dW; it0[m][r] = steps before run r.
-struct RunJobs {
-  int32_t n[2];
-  int32_t start[2][MF_MAX_SAMPLES];
-  int32_t len[2][MF_MAX_SAMPLES];
-  int32_t it0[2][MF_MAX_SAMPLES + 1];
-  int32_t units[2];   // output tiles x splits of the modality
-  int32_t splits[2];  // parts of the modality's steps
-  float* part;        // [units of split modalities][256][256], or NULL
-};
-
 // out[c] = the sum of part[k][c] over k, in order.
 struct ColumnSums {
   const float* part;
@@ -106,27 +92,53 @@ struct ColumnSums {
   float* out;
 };
 
-template <int MODE>
-struct JobsOf {
-  using type = RowJobs;
+// The column tiles of a product's output.
+struct Columns {
+  int32_t width;  // columns of a tile: a multiple of 16, at most 256
+  int32_t tiles;
+  int32_t nb;     // tiles per block of the traversal
 };
-template <>
-struct JobsOf<kDw> {
-  using type = RunJobs;
+
+struct FwdArgs {
+  GemmJobs jobs;   // one per (row block, modality present in it)
+  int32_t T, K, N;
+  Columns cols;
+  const uint8_t* tok_mod;
+  LinearEpilogue ep;
+  KernelCtl ctl;
+};
+
+// Kinds of the backward's units.
+constexpr int kDx = 0, kDwImage = 1;  // kDwImage + 1: dW of the text modality
+
+struct BwdArgs {
+  GemmJobs jobs;  // dx
+  // dW: the modalities' runs; it0[m][r] = steps before run r
+  int32_t n[2];
+  int32_t start[2][MF_MAX_SAMPLES];
+  int32_t len[2][MF_MAX_SAMPLES];
+  int32_t it0[2][MF_MAX_SAMPLES + 1];
+  int32_t splits[2];    // parts of the modality's steps
+  int32_t slot0[2];     // the modality's first slot of partial sums
+  float* part;          // [slots][256][256]
+  int32_t kind[3];      // the kinds in the queue's order, and where each ends in it
+  int32_t end[3];
+  int32_t T, K, N;
+  Columns dx_cols, dw_cols;
+  const uint8_t* tok_mod;
+  mf_bf16* dx;
+  mf_bf16* dW;
+  ColumnSums db;        // db's partials, or out NULL
+  KernelCtl ctl;
 };
 
 template <int MODE>
-struct Args {
-  typename JobsOf<MODE>::type j;
-  int32_t T, K, N;
-  int32_t n_steps;         // steps of the inner dimension (forward, dx)
-  int32_t width;           // columns of a tile: a multiple of 16, at most 256
-  int32_t col_tiles;       // column tiles of the output
-  int32_t nb;              // column tiles per block of the traversal
-  const uint8_t* tok_mod;
-  LinearEpilogue ep;       // forward: all of it; dx and dW: out
-  ColumnSums db;           // dx and dW: db's partials, or out NULL
-  KernelCtl ctl;
+struct ArgsOf {
+  using type = FwdArgs;
+};
+template <>
+struct ArgsOf<kBwd> {
+  using type = BwdArgs;
 };
 
 // Unit u -> (row tile or job, column tile): blocks of nb column tiles (the last
@@ -197,49 +209,77 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
 }
 
-// What a unit of dW covers: modality, tile, and steps [s0, s1) of its runs.
-struct DwUnit {
-  int m, nt, kt, s0, s1, slot;
+// What a unit covers. Forward and dx: row block, modality, column tile, all steps of
+// the inner dimension. dW: modality, row tile (blk), column tile, steps [s0, s0 +
+// steps) of the modality's runs (none without tokens), slot of its partial sums (-1:
+// dW itself).
+struct Unit {
+  bool dw;
+  int blk, m, ct, s0, steps, slot;
 };
-__device__ __forceinline__ DwUnit dw_unit(const Args<kDw>& a, int u) {
-  DwUnit w;
-  w.m = u < a.j.units[0] ? 0 : 1;
-  int i = w.m ? u - a.j.units[0] : u;
-  const int rows = (a.N + kTile - 1) / kTile;
-  const int tiles = rows * a.col_tiles;
-  const int part = i / tiles;
-  i -= part * tiles;
-  unit_coords(i, rows, a.col_tiles, a.nb, w.nt, w.kt);
-  const int total = a.j.it0[w.m][a.j.n[w.m]], p = a.j.splits[w.m];
-  w.s0 = static_cast<int>(static_cast<int64_t>(total) * part / p);
-  w.s1 = static_cast<int>(static_cast<int64_t>(total) * (part + 1) / p);
-  // slots of the image modality's parts come first
-  w.slot = p > 1 ? (w.m == 1 && a.j.splits[0] > 1 ? a.j.units[0] : 0) + part * tiles +
-                       w.nt * a.col_tiles + w.kt
-                 : -1;
+__device__ __forceinline__ Unit unit_of(const FwdArgs& a, int u) {
+  Unit w;
+  int ji;
+  unit_coords(u, a.jobs.n, a.cols.tiles, a.cols.nb, ji, w.ct);
+  const int job = a.jobs.job[ji];
+  w.dw = false;
+  w.blk = job & 0x7fff;
+  w.m = job >> 15;
+  w.s0 = 0;
+  w.steps = (a.K + kStepK - 1) / kStepK;
+  w.slot = -1;
   return w;
 }
-// The walk over a unit's steps: run and first row of the current one.
+__device__ __forceinline__ Unit unit_of(const BwdArgs& a, int u) {
+  Unit w;
+  const int q = (u >= a.end[0]) + (u >= a.end[1]);
+  const int kind = a.kind[q];
+  if (q > 0) u -= a.end[q - 1];
+  if (kind == kDx) {
+    int ji;
+    unit_coords(u, a.jobs.n, a.dx_cols.tiles, a.dx_cols.nb, ji, w.ct);
+    const int job = a.jobs.job[ji];
+    w.dw = false;
+    w.blk = job & 0x7fff;
+    w.m = job >> 15;
+    w.s0 = 0;
+    w.steps = (a.N + kStepK - 1) / kStepK;
+    w.slot = -1;
+    return w;
+  }
+  w.dw = true;
+  w.m = kind - kDwImage;
+  const int rows = (a.N + kTile - 1) / kTile;
+  const int tiles = rows * a.dw_cols.tiles;
+  const int part = u / tiles;
+  unit_coords(u - part * tiles, rows, a.dw_cols.tiles, a.dw_cols.nb, w.blk, w.ct);
+  const int total = a.it0[w.m][a.n[w.m]], p = a.splits[w.m];
+  w.s0 = static_cast<int>(static_cast<int64_t>(total) * part / p);
+  w.steps = static_cast<int>(static_cast<int64_t>(total) * (part + 1) / p) - w.s0;
+  w.slot = p > 1 ? a.slot0[w.m] + part * tiles + w.blk * a.dw_cols.tiles + w.ct : -1;
+  return w;
+}
+// The walk over a dW unit's steps: run and first row of the current one.
 struct RunWalk {
   int r, row, left;
-  __device__ __forceinline__ void start(const Args<kDw>& a, int m, int step) {
-    int lo = 0, hi = a.j.n[m] - 1;  // last run with it0 <= step
+  __device__ __forceinline__ void start(const BwdArgs& a, const Unit& w) {
+    int lo = 0, hi = a.n[w.m] - 1;  // last run with it0 <= s0
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (a.j.it0[m][mid] <= step) lo = mid; else hi = mid - 1;
+      if (a.it0[w.m][mid] <= w.s0) lo = mid; else hi = mid - 1;
     }
     r = lo;
-    const int off = (step - a.j.it0[m][r]) * kStepK;
-    row = a.j.start[m][r] + off;
-    left = a.j.len[m][r] - off;
+    const int off = (w.s0 - a.it0[w.m][r]) * kStepK;
+    row = a.start[w.m][r] + off;
+    left = a.len[w.m][r] - off;
   }
-  __device__ __forceinline__ void next(const Args<kDw>& a, int m) {
+  __device__ __forceinline__ void next(const BwdArgs& a, int m) {
     row += kStepK;
     left -= kStepK;
-    if (left <= 0 && r + 1 < a.j.n[m]) {
+    if (left <= 0 && r + 1 < a.n[m]) {
       ++r;
-      row = a.j.start[m][r];
-      left = a.j.len[m][r];
+      row = a.start[m][r];
+      left = a.len[m][r];
     }
   }
 };
@@ -337,7 +377,7 @@ __device__ __forceinline__ void store32_codes(int8_t* p, int left, const float (
 // their largest magnitude; z itself never reaches memory. bias: the tile's, in shared
 // memory, or NULL; res: the residual's first 32 columns, asked for before the
 // accumulator was waited for (each next 32 are asked for one step ahead).
-__device__ __forceinline__ void forward_row(const Args<kFwd>& a, uint32_t taddr, int t, bool keep,
+__device__ __forceinline__ void forward_row(const FwdArgs& a, uint32_t taddr, int t, bool keep,
                                             int n0, int cc0, int cc1, const float* bias,
                                             Resid32& res) {
   const LinearEpilogue& ep = a.ep;
@@ -381,11 +421,14 @@ __device__ __forceinline__ void forward_row(const Args<kFwd>& a, uint32_t taddr,
   }
 }
 
+// Maps: forward x, W; backward dz and W for dx, dz and x for dW (map_c, map_d).
 template <int MODE>
 __global__ void __launch_bounds__(kWarps * 32, 1)
     linear_fused_kernel(const __grid_constant__ CUtensorMap map_a,
                         const __grid_constant__ CUtensorMap map_b,
-                        const __grid_constant__ Args<MODE> args) {
+                        const __grid_constant__ CUtensorMap map_c,
+                        const __grid_constant__ CUtensorMap map_d, int units,
+                        const __grid_constant__ typename ArgsOf<MODE>::type args) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -416,82 +459,66 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int rank = static_cast<int>(cluster_ctarank());
   const int unit0 = static_cast<int>(blockIdx.x >> 1);
   const int stride = static_cast<int>(gridDim.x >> 1);
-  int units;
-  if constexpr (MODE == kDw)
-    units = args.j.units[0] + args.j.units[1];
-  else
-    units = args.j.jobs.n * args.col_tiles;
-
-  // Row tile, modality and column tile of a unit, and its steps.
-  auto row_job = [&](int u, int& blk, int& m, int& ct) {
-    if constexpr (MODE != kDw) {
-      int ji;
-      unit_coords(u, args.j.jobs.n, args.col_tiles, args.nb, ji, ct);
-      const int job = args.j.jobs.job[ji];
-      blk = job & 0x7fff;
-      m = job >> 15;
-    }
-  };
 
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t keep = keep_in_l2();
-      // This CTA's half of a tile's B columns; a strided B comes in boxes of 64.
-      const int half = args.width / 2;
-      const bool two = half > 64;
-      const uint32_t bytes =
-          kABytes + (MODE == kFwd ? half * kStepK * 2 : two ? 2 * kBoxBytes : kBoxBytes);
       uint32_t it = 0, part_uses = 0;  // bit st: parity of PART[st]'s uses
       uint32_t part_used = 0;          // bit st: used at all
       bool ok = true;
       for (int u = unit0; u < units && ok; u += stride) {
-        DwUnit w;
+        const Unit w = unit_of(args, u);
         RunWalk walk;
-        int blk = 0, m = 0, ct = 0, steps;
-        if constexpr (MODE == kDw) {
-          w = dw_unit(args, u);
-          steps = w.s1 - w.s0;
-          if (steps > 0) walk.start(args, w.m, w.s0);
+        // this CTA's half of the tile's B columns; a strided B comes in boxes of 64
+        int width;
+        if constexpr (MODE == kFwd) {
+          width = args.cols.width;
         } else {
-          row_job(u, blk, m, ct);
-          steps = args.n_steps;
+          width = w.dw ? args.dw_cols.width : args.dx_cols.width;
+          if (w.dw && w.steps > 0) walk.start(args, w);
         }
-        for (int s = 0; s < steps; ++s, ++it) {
+        const int half = width / 2;
+        const bool two = half > 64;
+        const uint32_t bytes =
+            kABytes + (MODE == kFwd ? half * kStepK * 2 : two ? 2 * kBoxBytes : kBoxBytes);
+        const int row = w.blk * kTile + rank * kHalf, col = w.ct * width + rank * half;
+        for (int s = 0; s < w.steps; ++s, ++it) {
           const int st = it % kStages;
           if (!(ok = mbar_wait(&bars[kEmpty + st], ((it / kStages) & 1) ^ 1, args.ctl, abort_flag)))
             break;
           uint8_t* sa = smem + st * kStageBytes;
           uint8_t* sb = sa + kABytes;
-          if constexpr (MODE == kDw) {
-            const int xa = w.nt * kTile + rank * kHalf, xb = w.kt * args.width + rank * half;
-            if (walk.left < kStepK) {
-              mbar_expect_tx(&bars[kPart + st], bytes);
-              tma_load_2d(sa, &map_a, &bars[kPart + st], xa, walk.row);
-              tma_load_2d(sa + kBoxBytes, &map_a, &bars[kPart + st], xa + 64, walk.row);
-              tma_load_2d(sb, &map_b, &bars[kPart + st], xb, walk.row);
-              if (two) tma_load_2d(sb + kBoxBytes, &map_b, &bars[kPart + st], xb + 64, walk.row);
-              part_uses ^= 1u << st;
-              part_used |= 1u << st;
-            } else {
-              const uint32_t bar = cluster_addr(&bars[kFull + st], 0);
-              expect_pair(bar, bytes);
-              tma_load_2d_pair(sa, &map_a, bar, xa, walk.row);
-              tma_load_2d_pair(sa + kBoxBytes, &map_a, bar, xa + 64, walk.row);
-              tma_load_2d_pair(sb, &map_b, bar, xb, walk.row);
-              if (two) tma_load_2d_pair(sb + kBoxBytes, &map_b, bar, xb + 64, walk.row);
+          if constexpr (MODE == kBwd) {
+            if (w.dw) {
+              if (walk.left < kStepK) {
+                uint64_t* bar = &bars[kPart + st];
+                mbar_expect_tx(bar, bytes);
+                tma_load_2d(sa, &map_c, bar, row, walk.row);
+                tma_load_2d(sa + kBoxBytes, &map_c, bar, row + 64, walk.row);
+                tma_load_2d(sb, &map_d, bar, col, walk.row);
+                if (two) tma_load_2d(sb + kBoxBytes, &map_d, bar, col + 64, walk.row);
+                part_uses ^= 1u << st;
+                part_used |= 1u << st;
+              } else {
+                const uint32_t bar = cluster_addr(&bars[kFull + st], 0);
+                expect_pair(bar, bytes);
+                tma_load_2d_pair(sa, &map_c, bar, row, walk.row);
+                tma_load_2d_pair(sa + kBoxBytes, &map_c, bar, row + 64, walk.row);
+                tma_load_2d_pair(sb, &map_d, bar, col, walk.row);
+                if (two) tma_load_2d_pair(sb + kBoxBytes, &map_d, bar, col + 64, walk.row);
+              }
+              walk.next(args, w.m);
+              continue;
             }
-            walk.next(args, w.m);
+          }
+          const uint32_t bar = cluster_addr(&bars[kFull + st], 0);
+          expect_pair(bar, bytes);
+          tma_load_2d_pair(sa, &map_a, bar, s * kStepK, row);
+          if constexpr (MODE == kFwd) {
+            load_w(sb, &map_b, bar, s * kStepK, col, w.m, keep);
           } else {
-            const int row = blk * kTile + rank * kHalf, col = ct * args.width + rank * half;
-            const uint32_t bar = cluster_addr(&bars[kFull + st], 0);
-            expect_pair(bar, bytes);
-            tma_load_2d_pair(sa, &map_a, bar, s * kStepK, row);
-            if constexpr (MODE == kFwd) {
-              load_w(sb, &map_b, bar, s * kStepK, col, m, keep);
-            } else {
-              load_w(sb, &map_b, bar, col, s * kStepK, m, keep);
-              if (two) load_w(sb + kBoxBytes, &map_b, bar, col + 64, s * kStepK, m, keep);
-            }
+            load_w(sb, &map_b, bar, col, s * kStepK, w.m, keep);
+            if (two) load_w(sb + kBoxBytes, &map_b, bar, col + 64, s * kStepK, w.m, keep);
           }
         }
       }
@@ -509,48 +536,49 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      constexpr int A_MN = MODE == kDw, B_MN = MODE != kFwd;
-      const uint32_t IDESC = idesc_bf16_f32(2 * kHalf, args.width, A_MN, B_MN);
-      // a 16-element step is 32 bytes along a contiguous inner dimension, 16 rows
-      // of 128 bytes along a strided one
-      constexpr uint64_t A_STEP = A_MN ? 128 : 2, B_STEP = B_MN ? 128 : 2;
       const uint32_t base = smem_u32(smem);
-      const uint64_t a_desc = sdesc_sw128(base, A_MN ? kBoxBytes : 16, 1024);
-      const uint64_t b_desc = sdesc_sw128(base + kABytes, B_MN ? kBoxBytes : 16, 1024);
+      // a contiguous inner dimension: 16 elements are 32 bytes; a strided one: 16 rows
+      // of 128 bytes, the 64-column boxes kBoxBytes apart
+      const uint64_t a_flat = sdesc_sw128(base, 16, 1024);
+      const uint64_t a_rows = sdesc_sw128(base, kBoxBytes, 1024);
+      const uint64_t b_desc = sdesc_sw128(base + kABytes, MODE == kFwd ? 16 : kBoxBytes, 1024);
+      constexpr uint64_t B_STEP = MODE == kFwd ? 2 : 128;
       uint32_t it = 0, ul = 0;
       bool ok = true;
       for (int u = unit0; u < units && ok; u += stride, ++ul) {
         const uint32_t acc = ul & 1;
         if (!mbar_wait(&bars[kAccEmpty + acc], ((ul >> 1) & 1) ^ 1, args.ctl, abort_flag)) break;
         tc_fence_after();
-        int steps, m = 0;
+        const Unit w = unit_of(args, u);
         RunWalk walk;
-        if constexpr (MODE == kDw) {
-          const DwUnit w = dw_unit(args, u);
-          m = w.m;
-          steps = w.s1 - w.s0;
-          if (steps > 0) walk.start(args, m, w.s0);
+        uint32_t idesc;
+        if constexpr (MODE == kFwd) {
+          idesc = idesc_bf16_f32(2 * kHalf, args.cols.width, 0, 0);
         } else {
-          steps = args.n_steps;
+          idesc = w.dw ? idesc_bf16_f32(2 * kHalf, args.dw_cols.width, 1, 1)
+                       : idesc_bf16_f32(2 * kHalf, args.dx_cols.width, 0, 1);
+          if (w.dw && w.steps > 0) walk.start(args, w);
         }
+        const uint64_t a_desc = w.dw ? a_rows : a_flat;
+        const uint64_t a_step = w.dw ? 128 : 2;
         const uint32_t d = tmem + acc * kTile;
-        for (int s = 0; s < steps; ++s, ++it) {
+        for (int s = 0; s < w.steps; ++s, ++it) {
           const int st = it % kStages;
           const uint32_t parity = (it / kStages) & 1;
-          if constexpr (MODE == kDw) {
-            // zeroed rows were written by threads of both CTAs
-            ok = walk.left < kStepK ? mbar_wait_cluster(&bars[kFull + st], parity, args.ctl, abort_flag)
-                                    : mbar_wait(&bars[kFull + st], parity, args.ctl, abort_flag);
-            walk.next(args, m);
-          } else {
-            ok = mbar_wait(&bars[kFull + st], parity, args.ctl, abort_flag);
-          }
+          bool zeroed = false;  // rows zeroed by threads of both CTAs
+          if constexpr (MODE == kBwd)
+            if (w.dw) {
+              zeroed = walk.left < kStepK;
+              walk.next(args, w.m);
+            }
+          ok = zeroed ? mbar_wait_cluster(&bars[kFull + st], parity, args.ctl, abort_flag)
+                      : mbar_wait(&bars[kFull + st], parity, args.ctl, abort_flag);
           if (!ok) break;
           tc_fence_after();
           const uint64_t so = static_cast<uint64_t>((st * kStageBytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < kStepK / 16; ++kk)
-            umma_ss_pair(d, a_desc + so + kk * A_STEP, b_desc + so + kk * B_STEP, IDESC,
+            umma_ss_pair(d, a_desc + so + kk * a_step, b_desc + so + kk * B_STEP, idesc,
                          (s > 0 || kk > 0) ? 1u : 0u);
           umma_commit_pair(&bars[kEmpty + st], 3);
         }
@@ -569,26 +597,25 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const int row = wq * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
     const int cc0 = warp >= 8 ? kTile / 2 : 0;
-    const int cc1 = warp >= 8 ? args.width : min(kTile / 2, args.width);
     uint32_t ul = 0;
     bool stop = false;  // a wait ran out: the forward's warps still meet at their barrier
     for (int u = unit0; u < units; u += stride, ++ul) {
       const uint32_t acc = ul & 1;
       const uint32_t taddr = tmem + lane_base + acc * kTile;
+      const Unit w = unit_of(args, u);
+      const int r = w.blk * kTile + rank * kHalf + row;  // token, or row of dW
       if constexpr (MODE == kFwd) {
-        int blk = 0, m = 0, ct = 0;
-        row_job(u, blk, m, ct);
-        const int t = blk * kTile + rank * kHalf + row, n0 = ct * args.width;
-        const bool keep = t < args.T && __ldg(args.tok_mod + t) == m;
-        const int end = min(cc1, args.N - n0);
+        const int n0 = w.ct * args.cols.width;
+        const bool keep = r < args.T && __ldg(args.tok_mod + r) == w.m;
+        const int end = min(min(cc0 + kTile / 2, args.cols.width), args.N - n0);
         float* bias = reinterpret_cast<float*>(smem + kOffBias);
         Resid32 res;
         if (args.ep.resid != nullptr && keep && cc0 < end)
-          res.load(args.ep.resid + static_cast<size_t>(t) * args.N + n0 + cc0, end - cc0);
+          res.load(args.ep.resid + static_cast<size_t>(r) * args.N + n0 + cc0, end - cc0);
         if (args.ep.bias != nullptr) {
           const int c = static_cast<int>(threadIdx.x) - 4 * 32;
           const float v = n0 + c < args.N
-                              ? __ldg(args.ep.bias + static_cast<size_t>(m) * args.N + n0 + c)
+                              ? __ldg(args.ep.bias + static_cast<size_t>(w.m) * args.N + n0 + c)
                               : 0.f;
           epilogue_sync();  // every warp is done with the tile before
           bias[c] = v;
@@ -597,49 +624,41 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         if (!warp_wait(&bars[kAccFull + acc], (ul >> 1) & 1, args.ctl, abort_flag)) stop = true;
         tc_fence_after();
         if (!stop)
-          forward_row(args, taddr, t, keep, n0, cc0, end, args.ep.bias != nullptr ? bias : nullptr,
+          forward_row(args, taddr, r, keep, n0, cc0, end, args.ep.bias != nullptr ? bias : nullptr,
                       res);
       } else {
-        if (!warp_wait(&bars[kAccFull + acc], (ul >> 1) & 1, args.ctl, abort_flag)) break;
-        tc_fence_after();
-        int k0;
+        const int width = w.dw ? args.dw_cols.width : args.dx_cols.width;
+        const int k0 = w.ct * width;
+        const int end = min(min(cc0 + kTile / 2, width), args.K - k0);
         bool keep;
         mf_bf16* out;
         float* part = nullptr;
-        bool none = false;  // dW of a modality without tokens
-        if constexpr (MODE == kDw) {
-          const DwUnit w = dw_unit(args, u);
-          const int n = w.nt * kTile + rank * kHalf + row;
-          k0 = w.kt * args.width;
-          keep = n < args.N;
-          none = w.s0 == w.s1;
-          out = args.ep.out + (static_cast<size_t>(w.m) * args.N + n) * args.K + k0;
+        if (w.dw) {
+          keep = r < args.N;
+          out = args.dW + (static_cast<size_t>(w.m) * args.N + r) * args.K + k0;
           if (w.slot >= 0)
-            part = args.j.part +
+            part = args.part +
                    (static_cast<size_t>(w.slot) * kTile + rank * kHalf + row) * kTile;
         } else {
-          int blk = 0, m = 0, ct = 0;
-          row_job(u, blk, m, ct);
-          const int t = blk * kTile + rank * kHalf + row;
-          k0 = ct * args.width;
-          keep = t < args.T && __ldg(args.tok_mod + t) == m;
-          out = args.ep.out + static_cast<size_t>(t) * args.K + k0;
+          keep = r < args.T && __ldg(args.tok_mod + r) == w.m;
+          out = args.dx + static_cast<size_t>(r) * args.K + k0;
         }
-        const int end = min(cc1, args.K - k0);
+        if (!warp_wait(&bars[kAccFull + acc], (ul >> 1) & 1, args.ctl, abort_flag)) break;
+        tc_fence_after();
 #pragma unroll 1
         for (int cc = cc0; cc < end; cc += 32) {
           float f[32];
           acc_load32(taddr + cc, f);
-          if (none)
+          if (w.steps == 0)  // dW of a modality without tokens
 #pragma unroll
             for (int e = 0; e < 32; ++e) f[e] = 0.f;
           if (part != nullptr) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              uint32_t r[8];
+              uint32_t v[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) r[e] = __float_as_uint(f[8 * q + e]);
-              store_sector(part + cc + 8 * q, r);
+              for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(f[8 * q + e]);
+              store_sector(part + cc + 8 * q, v);
             }
           } else if (keep) {
             store32(out + cc, end - cc, f);
@@ -650,27 +669,33 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(cluster_addr(&bars[kAccEmpty + acc], 0));
     }
-  } else if (MODE != kFwd && warp == 3) {
-    if (args.db.out != nullptr) {
-      for (int c = static_cast<int>(blockIdx.x) * 32 + lane; c < args.db.cols;
-           c += static_cast<int>(gridDim.x) * 32) {
-        float v = 0.f;
+  } else if (MODE == kBwd && warp == 3) {
+    if constexpr (MODE == kBwd) {
+      if (args.db.out != nullptr) {
+        for (int c = static_cast<int>(blockIdx.x) * 32 + lane; c < args.db.cols;
+             c += static_cast<int>(gridDim.x) * 32) {
+          float v = 0.f;
 #pragma unroll 8
-        for (int k = 0; k < args.db.n; ++k)
-          v += __ldcg(args.db.part + static_cast<size_t>(k) * args.db.cols + c);
-        args.db.out[c] = v;
+          for (int k = 0; k < args.db.n; ++k)
+            v += __ldcg(args.db.part + static_cast<size_t>(k) * args.db.cols + c);
+          args.db.out[c] = v;
+        }
       }
     }
-  } else if (MODE == kDw && warp == 2) {
-    if constexpr (MODE == kDw) {
+  } else if (MODE == kBwd && warp == 2) {
+    if constexpr (MODE == kBwd) {
       uint32_t it = 0, part_uses = 0;
       bool ok = true;
       for (int u = unit0; u < units && ok; u += stride) {
-        const DwUnit w = dw_unit(args, u);
-        if (w.s0 == w.s1) continue;
+        const Unit w = unit_of(args, u);
+        if (!w.dw) {
+          it += w.steps;
+          continue;
+        }
+        if (w.steps == 0) continue;
         RunWalk walk;
-        walk.start(args, w.m, w.s0);
-        for (int s = w.s0; s < w.s1; ++s, ++it, walk.next(args, w.m)) {
+        walk.start(args, w);
+        for (int s = 0; s < w.steps; ++s, ++it, walk.next(args, w.m)) {
           const int live = walk.left;
           if (live >= kStepK) continue;
           const int st = it % kStages;
@@ -910,13 +935,13 @@ int max_clusters() {
 }
 
 template <int MODE>
-cudaError_t launch_product(const CUtensorMap& ma, const CUtensorMap& mb, const Args<MODE>& a,
+cudaError_t launch_product(const CUtensorMap (&m)[4], const typename ArgsOf<MODE>::type& a,
                            int units, cudaStream_t st) {
   const int mc = max_clusters<MODE>();
   if (mc <= 0) return cudaErrorInvalidConfiguration;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = config<MODE>(units < mc ? units : mc, attr, st);
-  return cudaLaunchKernelEx(&cfg, linear_fused_kernel<MODE>, ma, mb, a);
+  return cudaLaunchKernelEx(&cfg, linear_fused_kernel<MODE>, m[0], m[1], m[2], m[3], units, a);
 }
 
 int tiles_of(int64_t v) { return static_cast<int>((v + kTile - 1) / kTile); }
@@ -966,17 +991,10 @@ int forward_width(int rows, int cols, int pairs, bool blocks) {
   return best;
 }
 
-template <int MODE>
-void fill(Args<MODE>& a, int32_t T, int32_t K, int32_t N, int cols, int width,
-          const KernelCtl& ctl) {
-  a.T = T;
-  a.K = K;
-  a.N = N;
-  a.width = width;
-  a.col_tiles = (cols + width - 1) / width;
-  a.nb = a.col_tiles < 12 ? a.col_tiles : 12;
-  a.db = ColumnSums{};
-  a.ctl = ctl;
+Columns columns(int cols, int width) {
+  while (width > 64 && width / 2 >= cols) width /= 2;  // no wider than the output
+  const int tiles = (cols + width - 1) / width;
+  return Columns{width, tiles, tiles < 12 ? tiles : 12};
 }
 
 // Pairs of SMs on a B200 (148 SMs): what dW's split and its workspace are sized by.
@@ -1052,16 +1070,21 @@ cudaError_t launch_linear_fused(const mf_bf16* x, const mf_bf16* W, const TokenR
                                 const uint8_t* tok_mod, int32_t T, int32_t K, int32_t N,
                                 const LinearEpilogue& ep, const KernelCtl& ctl, cudaStream_t st) {
   if (few_rows(T)) return launch_linear_rows(x, W, runs, tok_mod, T, K, N, ep, ctl, st);
-  static thread_local Args<kFwd> a;
-  row_jobs(runs, T, &a.j.jobs);
-  fill(a, T, K, N, N, forward_width(a.j.jobs.n, N, max_clusters<kFwd>(), ep.z8 != nullptr), ctl);
-  CUtensorMap ma, mb;
-  if (!linear_map(&ma, x, K, T, 0, kHalf) || !linear_map(&mb, W, K, N, 2, a.width / 2))
-    return cudaErrorInvalidValue;
-  a.n_steps = (K + kStepK - 1) / kStepK;
+  static thread_local FwdArgs a;
+  row_jobs(runs, T, &a.jobs);
+  a.T = T;
+  a.K = K;
+  a.N = N;
+  a.cols = columns(N, forward_width(a.jobs.n, N, max_clusters<kFwd>(), ep.z8 != nullptr));
   a.tok_mod = tok_mod;
   a.ep = ep;
-  return launch_product<kFwd>(ma, mb, a, a.j.jobs.n * a.col_tiles, st);
+  a.ctl = ctl;
+  CUtensorMap m[4];
+  if (!linear_map(&m[0], x, K, T, 0, kHalf) ||
+      !linear_map(&m[1], W, K, N, 2, a.cols.width / 2))
+    return cudaErrorInvalidValue;
+  m[2] = m[3] = m[0];
+  return launch_product<kFwd>(m, a, a.jobs.n * a.cols.tiles, st);
 }
 
 // Workspace, in this order: dz [T][N] bf16; db's partials; an 8-bit x in bf16; dW's
@@ -1112,63 +1135,86 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
     if (e != cudaSuccess) return e;
   }
 
-  if (b.dx != nullptr && few_rows(T)) {
+  const bool few_dx = b.dx != nullptr && few_rows(T);
+  if (few_dx) {
     e = launch_linear_rows_dx(dz, b.W, runs, b.tok_mod, T, K, N, b.dx, ctl, st);
     if (e != cudaSuccess) return e;
-  } else if (b.dx != nullptr) {
-    CUtensorMap ma, mb;
-    if (!linear_map(&ma, dz, N, T, 0, kHalf) ||
-        !linear_map(&mb, b.W, K, N, 2, kStepK))
-      return cudaErrorInvalidValue;
-    static thread_local Args<kDx> a;
-    row_jobs(runs, T, &a.j.jobs);
-    fill(a, T, K, N, K, tile_width(a.j.jobs.n, K, max_clusters<kDx>(), 64), ctl);
-    a.n_steps = (N + kStepK - 1) / kStepK;
-    a.tok_mod = b.tok_mod;
-    a.ep = LinearEpilogue{};
-    a.ep.out = b.dx;
-    a.db = db;
-    db.out = nullptr;
-    e = launch_product<kDx>(ma, mb, a, a.j.jobs.n * a.col_tiles, st);
-    if (e != cudaSuccess) return e;
   }
-
-  if (b.dW != nullptr) {
-    const mf_bf16* x = b.x != nullptr ? b.x : x_ws;
-    CUtensorMap ma, mb;
-    if (!linear_map(&ma, dz, N, T, 0, kStepK) || !linear_map(&mb, x, K, T, 0, kStepK))
-      return cudaErrorInvalidValue;
-    static thread_local Args<kDw> a;
-    fill(a, T, K, N, K, dw_width(K, N), ctl);
-    a.ep = LinearEpilogue{};
-    a.ep.out = b.dW;
+  if ((b.dx != nullptr && !few_dx) || b.dW != nullptr) {
+    static thread_local BwdArgs a;
+    a.T = T;
+    a.K = K;
+    a.N = N;
+    a.tok_mod = b.tok_mod;
+    a.dx = b.dx;
+    a.dW = b.dW;
+    a.part = dw_part;
     a.db = db;
+    a.ctl = ctl;
     db.out = nullptr;
-    a.j.part = dw_part;
-    const int tiles = tiles_of(N) * a.col_tiles;
-    for (int m = 0; m < 2; ++m) {
-      a.j.n[m] = runs.n[m];
-      a.j.it0[m][0] = 0;
-      for (int r = 0; r < runs.n[m]; ++r) {
-        a.j.start[m][r] = runs.start[m][r];
-        a.j.len[m][r] = runs.len[m][r];
-        a.j.it0[m][r + 1] = a.j.it0[m][r] + (runs.len[m][r] + kStepK - 1) / kStepK;
-      }
-      a.j.splits[m] = dw_splits(tiles, a.j.it0[m][runs.n[m]]);
-      a.j.units[m] = tiles * a.j.splits[m];
+    CUtensorMap m[4];
+    int units[3] = {0, 0, 0};
+    int64_t cost[3] = {0, 0, 0};  // of a unit, by kind
+    a.jobs.n = 0;
+    a.dx_cols = a.dw_cols = columns(K, kTile);
+    if (b.dx != nullptr && !few_dx) {
+      if (!linear_map(&m[0], dz, N, T, 0, kHalf) || !linear_map(&m[1], b.W, K, N, 2, kStepK))
+        return cudaErrorInvalidValue;
+      row_jobs(runs, T, &a.jobs);
+      // narrower tiles where they fill SMs that nothing else would
+      a.dx_cols = columns(
+          K, b.dW != nullptr ? kTile : tile_width(a.jobs.n, K, max_clusters<kBwd>(), 64));
+      units[kDx] = a.jobs.n * a.dx_cols.tiles;
+      cost[kDx] = static_cast<int64_t>((N + kStepK - 1) / kStepK) * a.dx_cols.width;
     }
-    const int units = a.j.units[0] + a.j.units[1];
-    e = launch_product<kDw>(ma, mb, a, units, st);
+    const int dw_width_ = dw_width(K, N);
+    int slots = 0;
+    if (b.dW != nullptr) {
+      if (!linear_map(&m[2], dz, N, T, 0, kStepK) ||
+          !linear_map(&m[3], b.x != nullptr ? b.x : x_ws, K, T, 0, kStepK))
+        return cudaErrorInvalidValue;
+      a.dw_cols = columns(K, dw_width_);
+      const int tiles = tiles_of(N) * a.dw_cols.tiles;
+      for (int i = 0; i < 2; ++i) {
+        a.n[i] = runs.n[i];
+        a.it0[i][0] = 0;
+        for (int r = 0; r < runs.n[i]; ++r) {
+          a.start[i][r] = runs.start[i][r];
+          a.len[i][r] = runs.len[i][r];
+          a.it0[i][r + 1] = a.it0[i][r] + (runs.len[i][r] + kStepK - 1) / kStepK;
+        }
+        const int steps = a.it0[i][runs.n[i]];
+        a.splits[i] = dw_splits(tiles, steps);
+        a.slot0[i] = slots;
+        units[kDwImage + i] = tiles * a.splits[i];
+        if (a.splits[i] > 1) slots += units[kDwImage + i];
+        cost[kDwImage + i] = static_cast<int64_t>(steps / a.splits[i]) * dw_width_;
+      }
+    }
+    if (b.dx == nullptr || few_dx) m[0] = m[1] = m[2];
+    if (b.dW == nullptr) m[2] = m[3] = m[0];
+    // the queue: the kind with the longest units first
+    int total = 0;
+    bool queued[3] = {false, false, false};
+    for (int q = 0; q < 3; ++q) {
+      int best = -1;
+      for (int k = 0; k < 3; ++k)
+        if (!queued[k] && (best < 0 || cost[k] > cost[best])) best = k;
+      queued[best] = true;
+      a.kind[q] = best;
+      a.end[q] = total += units[best];
+    }
+    e = launch_product<kBwd>(m, a, total, st);
     if (e != cudaSuccess) return e;
-    float* part = dw_part;
-    for (int m = 0; m < 2; ++m) {
-      if (a.j.splits[m] == 1) continue;
+    for (int i = 0; i < 2 && b.dW != nullptr; ++i) {
+      if (a.splits[i] == 1) continue;
       const int64_t groups = static_cast<int64_t>(N) * (K / 8);
       e = launch_dependent(dw_parts_kernel, dim3(static_cast<unsigned>((groups + 255) / 256)),
-                           dim3(256), 0, st, part, a.j.splits[m], N, K, a.width, a.col_tiles,
-                           tiles, b.dW + static_cast<size_t>(m) * N * K);
+                           dim3(256), 0, st,
+                           dw_part + static_cast<size_t>(a.slot0[i]) * kTile * kTile, a.splits[i],
+                           N, K, a.dw_cols.width, a.dw_cols.tiles,
+                           tiles_of(N) * a.dw_cols.tiles, b.dW + static_cast<size_t>(i) * N * K);
       if (e != cudaSuccess) return e;
-      part += static_cast<size_t>(a.j.units[m]) * kTile * kTile;
     }
   }
   if (db.out != nullptr)
