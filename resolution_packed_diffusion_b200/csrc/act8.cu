@@ -10,10 +10,9 @@
 // Infrastructure) names training under a memory budget; the format is this
 // library's own.
 //
-// Both kernels are bound by HBM (3 bytes a value plus the scales). Sixteen lanes
-// hold a block, eight channels (16 bytes) each, so two blocks to a warp and a
-// maximum by four shuffles; every thread takes kUnroll blocks whose loads are all
-// issued before the first is used.
+// Both kernels are bound by HBM (3 bytes a value plus the scales): 0.76 of it stored,
+// 0.9 read back at 16384 x 3072. A block's lanes find its maximum by shuffles and
+// share its two divisions (act8.cuh).
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -26,11 +25,6 @@ namespace mf {
 
 namespace {
 
-constexpr int kThreads = kAct8Threads;
-constexpr int kUnroll = kAct8Unroll;
-constexpr int kLanes = kAct8Lanes;
-constexpr int kPerCta = kAct8PerCta;
-
 // Largest |x| of eight bf16 values as a 15-bit pattern (NaN above infinity).
 __device__ __forceinline__ uint32_t absmax_bits(const uint4& u) {
   const uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
@@ -38,63 +32,77 @@ __device__ __forceinline__ uint32_t absmax_bits(const uint4& u) {
   return max(m & 0xFFFFu, m >> 16);
 }
 
-__global__ void __launch_bounds__(kThreads) act8_quantize_kernel(const mf_bf16* __restrict__ x,
-                                                                 const Act8Rows rows,
-                                                                 int8_t* __restrict__ q,
-                                                                 float* __restrict__ scale) {
+template <bool WIDE>
+__global__ void __launch_bounds__(kAct8Threads)
+    act8_quantize_kernel(const mf_bf16* __restrict__ x, const Act8Rows rows,
+                         int8_t* __restrict__ q, float* __restrict__ scale) {
+  using S = Act8Shape<WIDE>;
   pdl_wait();
   pdl_release();
-  const int lane = threadIdx.x % kLanes;
-  const uint32_t base = blockIdx.x * (kPerCta * kUnroll) + threadIdx.x / kLanes;
-  uint4 v[kUnroll];
-  int64_t off[kUnroll];
-  bool in[kUnroll];
+  const int lane = threadIdx.x % S::LANES;
+  const uint32_t base = blockIdx.x * (S::PER_CTA * kAct8Unroll) + threadIdx.x / S::LANES;
+  uint4 v[kAct8Unroll], w[kAct8Unroll];
+  int64_t off[kAct8Unroll];
+  bool in[kAct8Unroll];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const uint32_t item = base + u * kPerCta;
+  for (int u = 0; u < kAct8Unroll; ++u) {
+    const uint32_t item = base + u * S::PER_CTA;
     const uint32_t row = rows.nb.div(item);
-    const int c = static_cast<int>(item - row * rows.nb.d) * kAct8Block + lane * 8;
+    const int c = static_cast<int>(item - row * rows.nb.d) * kAct8Block + lane * S::PER_LANE;
     in[u] = item < rows.items && c < rows.C;
     off[u] = static_cast<int64_t>(row) * rows.C + c;
-    v[u] = in[u] ? __ldcs(reinterpret_cast<const uint4*>(x + off[u])) : make_uint4(0, 0, 0, 0);
+    v[u] = w[u] = make_uint4(0, 0, 0, 0);
+    if (in[u]) {
+      if constexpr (WIDE)
+        load_sector(x + off[u], v[u], w[u]);
+      else
+        v[u] = __ldcs(reinterpret_cast<const uint4*>(x + off[u]));
+    }
   }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < kAct8Unroll; ++u) {
     uint32_t m = absmax_bits(v[u]);
+    if constexpr (WIDE) m = max(m, absmax_bits(w[u]));
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = S::LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     float s, inv;
     uint64_t f[4];
     act8_scale_pairwise(__uint_as_float(m << 16), lane & 1, s, inv);
     const uint32_t mask = inv == 0.f ? 0u : 0xFFFFFFFFu;
     bf16x8_f2(v[u], f);
-    if (in[u])
-      __stcs(reinterpret_cast<uint2*>(q + off[u]),
-             make_uint2(act8_code4(f[0], f[1], inv, mask), act8_code4(f[2], f[3], inv, mask)));
-    const uint32_t item = base + u * kPerCta;
+    const uint2 a = make_uint2(act8_code4(f[0], f[1], inv, mask), act8_code4(f[2], f[3], inv, mask));
+    if constexpr (WIDE) {
+      bf16x8_f2(w[u], f);
+      const uint2 b = make_uint2(act8_code4(f[0], f[1], inv, mask), act8_code4(f[2], f[3], inv, mask));
+      if (in[u]) __stcs(reinterpret_cast<uint4*>(q + off[u]), make_uint4(a.x, a.y, b.x, b.y));
+    } else {
+      if (in[u]) __stcs(reinterpret_cast<uint2*>(q + off[u]), a);
+    }
+    const uint32_t item = base + u * S::PER_CTA;
     if (lane == 0 && item < rows.items) scale[item] = s;
   }
 }
 
-template <int ACT>
-__global__ void __launch_bounds__(kThreads) act8_dequantize_kernel(const int8_t* __restrict__ q,
-                                                                   const float* __restrict__ scale,
-                                                                   const Act8Rows rows,
-                                                                   mf_bf16* __restrict__ y) {
+template <int ACT, bool WIDE>
+__global__ void __launch_bounds__(kAct8Threads)
+    act8_dequantize_kernel(const int8_t* __restrict__ q, const float* __restrict__ scale,
+                           const Act8Rows rows, mf_bf16* __restrict__ y) {
   pdl_wait();
   pdl_release();
-  act8_decode<ACT>(q, scale, rows, y, blockIdx.x);
+  act8_decode<ACT, WIDE>(q, scale, rows, y, blockIdx.x);
 }
 
 }  // namespace
 
 cudaError_t launch_act8_quantize(const mf_bf16* x, int32_t T, int32_t C, int8_t* q, float* scale,
                                  cudaStream_t st) {
+  const bool wide = act8_wide(x, C);
+  auto kernel = wide ? act8_quantize_kernel<true> : act8_quantize_kernel<false>;
   for (int32_t t = 0, n; t < T; t += n) {
     n = T - t < act8_rows_max(C) ? T - t : act8_rows_max(C);
     const Act8Rows rows = act8_rows(n, C);
     const cudaError_t e = launch_dependent(
-        act8_quantize_kernel, dim3(act8_decode_blocks(rows.items)), dim3(kThreads), 0, st,
+        kernel, dim3(act8_ctas(rows.items, wide)), dim3(kAct8Threads), 0, st,
         x + static_cast<size_t>(t) * C, rows, q + static_cast<size_t>(t) * C,
         scale + static_cast<size_t>(t) * act8_blocks(C));
     if (e != cudaSuccess) return e;
@@ -104,14 +112,18 @@ cudaError_t launch_act8_quantize(const mf_bf16* x, int32_t T, int32_t C, int8_t*
 
 cudaError_t launch_act8_dequantize(const int8_t* q, const float* scale, int32_t T, int32_t C,
                                    int32_t act, mf_bf16* y, cudaStream_t st) {
-  auto kernel = act == MF_ACT_GELU   ? act8_dequantize_kernel<MF_ACT_GELU>
-                : act == MF_ACT_SILU ? act8_dequantize_kernel<MF_ACT_SILU>
-                                     : act8_dequantize_kernel<MF_ACT_NONE>;
+  const bool wide = act8_wide(y, C);
+  auto kernel =
+      act == MF_ACT_GELU
+          ? (wide ? act8_dequantize_kernel<MF_ACT_GELU, true> : act8_dequantize_kernel<MF_ACT_GELU, false>)
+      : act == MF_ACT_SILU
+          ? (wide ? act8_dequantize_kernel<MF_ACT_SILU, true> : act8_dequantize_kernel<MF_ACT_SILU, false>)
+          : (wide ? act8_dequantize_kernel<MF_ACT_NONE, true> : act8_dequantize_kernel<MF_ACT_NONE, false>);
   for (int32_t t = 0, n; t < T; t += n) {
     n = T - t < act8_rows_max(C) ? T - t : act8_rows_max(C);
     const Act8Rows rows = act8_rows(n, C);
     const cudaError_t e = launch_dependent(
-        kernel, dim3(act8_decode_blocks(rows.items)), dim3(kThreads), 0, st,
+        kernel, dim3(act8_ctas(rows.items, wide)), dim3(kAct8Threads), 0, st,
         q + static_cast<size_t>(t) * C, scale + static_cast<size_t>(t) * act8_blocks(C), rows,
         y + static_cast<size_t>(t) * C);
     if (e != cudaSuccess) return e;

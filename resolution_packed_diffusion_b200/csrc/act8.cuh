@@ -184,15 +184,25 @@ __device__ __forceinline__ uint64_t act_grad2(uint64_t z) {
   return f2_fma(zd, f2_fma(f2_mul(s, f2_both(-1.f)), s, s), s);
 }
 
-// One CTA's share (256 threads) of y = act(q s): blocks of 128 channels, sixteen
-// lanes each, kAct8Unroll of them per thread with all loads issued first.
+// The checkpoint kernels: CTAs of 256 threads, sixteen lanes to a block of 128
+// channels with eight each, or (WIDE) eight lanes with sixteen each, where every row
+// starts on a 32-byte boundary of the bf16 tensor: half the loads, stores, shuffles
+// and divisions a value (store and read back at 16384 x 12288: 217 -> 200 us).
+// kAct8Unroll blocks per thread, all loads issued before the first is used.
 constexpr int kAct8Threads = 256;
 constexpr int kAct8Unroll = 4;
-constexpr int kAct8Lanes = kAct8Block / 8;
-constexpr int kAct8PerCta = kAct8Threads / kAct8Lanes;  // blocks a CTA takes per step
-
-inline unsigned act8_decode_blocks(uint32_t items) {
-  return (items + kAct8PerCta * kAct8Unroll - 1) / (kAct8PerCta * kAct8Unroll);
+template <bool WIDE>
+struct Act8Shape {
+  static constexpr int PER_LANE = WIDE ? 16 : 8;
+  static constexpr int LANES = kAct8Block / PER_LANE;
+  static constexpr int PER_CTA = kAct8Threads / LANES;  // blocks a CTA takes per step
+};
+inline unsigned act8_ctas(uint32_t items, bool wide) {
+  const uint32_t per = (wide ? Act8Shape<true>::PER_CTA : Act8Shape<false>::PER_CTA) * kAct8Unroll;
+  return (items + per - 1) / per;
+}
+inline bool act8_wide(const void* bf16_rows, int32_t C) {
+  return C % 16 == 0 && (reinterpret_cast<uintptr_t>(bf16_rows) & 31u) == 0;
 }
 
 // n / d for n < 2^31 by one high product (Granlund and Montgomery's method): with
@@ -222,33 +232,63 @@ inline Act8Rows act8_rows(int32_t T, int32_t C) {
   return Act8Rows{fast_div(nb), C, static_cast<uint32_t>(T) * nb};
 }
 
-template <int ACT>
+__device__ __forceinline__ void load_sector(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z),
+                 "=r"(b.w)
+               : "l"(p));
+}
+__device__ __forceinline__ void store_sector(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
+               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
+// One CTA's share of y = act(q s).
+template <int ACT, bool WIDE>
 __device__ __forceinline__ void act8_decode(const int8_t* __restrict__ q,
                                             const float* __restrict__ scale, const Act8Rows& rows,
                                             mf_bf16* __restrict__ y, uint32_t block) {
-  const int lane = threadIdx.x % kAct8Lanes;
-  const uint32_t base = block * (kAct8PerCta * kAct8Unroll) + threadIdx.x / kAct8Lanes;
-  uint2 v[kAct8Unroll];
+  using S = Act8Shape<WIDE>;
+  const int lane = threadIdx.x % S::LANES;
+  const uint32_t base = block * (S::PER_CTA * kAct8Unroll) + threadIdx.x / S::LANES;
+  uint4 v[kAct8Unroll];
   float s[kAct8Unroll];
   int64_t off[kAct8Unroll];
   bool in[kAct8Unroll];
 #pragma unroll
   for (int u = 0; u < kAct8Unroll; ++u) {
-    const uint32_t item = base + u * kAct8PerCta;
+    const uint32_t item = base + u * S::PER_CTA;
     const uint32_t row = rows.nb.div(item);
-    const int c = static_cast<int>(item - row * rows.nb.d) * kAct8Block + lane * 8;
+    const int c = static_cast<int>(item - row * rows.nb.d) * kAct8Block + lane * S::PER_LANE;
     in[u] = item < rows.items && c < rows.C;
     off[u] = static_cast<int64_t>(row) * rows.C + c;
-    v[u] = in[u] ? __ldcs(reinterpret_cast<const uint2*>(q + off[u])) : make_uint2(0, 0);
+    v[u] = make_uint4(0, 0, 0, 0);
+    if (in[u]) {
+      if constexpr (WIDE) {
+        v[u] = __ldcs(reinterpret_cast<const uint4*>(q + off[u]));
+      } else {
+        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(q + off[u]));
+        v[u].x = w.x;
+        v[u].y = w.y;
+      }
+    }
     s[u] = item < rows.items ? __ldg(scale + item) : 0.f;
   }
 #pragma unroll
   for (int u = 0; u < kAct8Unroll; ++u) {
-    uint64_t f[4];
-    act8_load(v[u], s[u], f);
+    uint64_t f[4], g[4];
+    act8_load(make_uint2(v[u].x, v[u].y), s[u], f);
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] = act_fwd2<ACT>(f[e]);
-    if (in[u]) __stcs(reinterpret_cast<uint4*>(y + off[u]), f2_bf16x8(f));
+    if constexpr (WIDE) {
+      act8_load(make_uint2(v[u].z, v[u].w), s[u], g);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) g[e] = act_fwd2<ACT>(g[e]);
+      if (in[u]) store_sector(y + off[u], f2_bf16x8(f), f2_bf16x8(g));
+    } else {
+      if (in[u]) __stcs(reinterpret_cast<uint4*>(y + off[u]), f2_bf16x8(f));
+    }
   }
 }
 

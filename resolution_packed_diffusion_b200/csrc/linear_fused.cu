@@ -326,10 +326,8 @@ struct Resid32 {
 
 // A thread stores runs of its own row, so a warp's store touches 32 rows: with 32
 // bytes a thread it writes whole sectors; with 16 it would write half of each, twice.
-__device__ __forceinline__ void store_sector(void* p, const uint32_t (&r)[8]) {
-  asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
+__device__ __forceinline__ void store_sector8(void* p, const uint32_t (&r)[8]) {
+  store_sector(p, make_uint4(r[0], r[1], r[2], r[3]), make_uint4(r[4], r[5], r[6], r[7]));
 }
 __device__ __forceinline__ bool sector_aligned(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 31u) == 0;
@@ -344,7 +342,7 @@ __device__ __forceinline__ void store32(mf_bf16* p, int left, const float (&f)[3
 #pragma unroll
     for (int e = 0; e < 8; ++e) r[e] = pack_bf16x2(f[16 * q + 2 * e], f[16 * q + 2 * e + 1]);
     if (wide && left >= 16 * (q + 1)) {
-      store_sector(p + 16 * q, r);
+      store_sector8(p + 16 * q, r);
     } else {
       if (left > 16 * q)
         __stcs(reinterpret_cast<uint4*>(p + 16 * q), make_uint4(r[0], r[1], r[2], r[3]));
@@ -362,7 +360,7 @@ __device__ __forceinline__ void store32_codes(int8_t* p, int left, const float (
   for (int e = 0; e < 8; ++e)
     r[e] = act8_code4(f2_pack(f[4 * e], f[4 * e + 1]), f2_pack(f[4 * e + 2], f[4 * e + 3]), inv, mask);
   if (left >= 32 && sector_aligned(p)) {
-    store_sector(p, r);
+    store_sector8(p, r);
   } else {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -658,7 +656,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
               uint32_t v[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(f[8 * q + e]);
-              store_sector(part + cc + 8 * q, v);
+              store_sector8(part + cc + 8 * q, v);
             }
           } else if (keep) {
             store32(out + cc, end - cc, f);
@@ -766,6 +764,7 @@ struct Decode {
   Act8 x8;
   Act8Rows rows;  // no items: nothing to decode
   mf_bf16* y;
+  bool wide;
 };
 
 template <int ACT, bool Z8>
@@ -779,7 +778,10 @@ __global__ void __launch_bounds__(256) dz_kernel(const mf_bf16* __restrict__ dou
   pdl_wait();
   pdl_release();
   if (static_cast<int>(blockIdx.x) >= dz_blocks) {
-    act8_decode<MF_ACT_NONE>(dec.x8.q, dec.x8.scale, dec.rows, dec.y, blockIdx.x - dz_blocks);
+    if (dec.wide)
+      act8_decode<MF_ACT_NONE, true>(dec.x8.q, dec.x8.scale, dec.rows, dec.y, blockIdx.x - dz_blocks);
+    else
+      act8_decode<MF_ACT_NONE, false>(dec.x8.q, dec.x8.scale, dec.rows, dec.y, blockIdx.x - dz_blocks);
     return;
   }
   const int chunk = blockIdx.x / col_blocks, cb = blockIdx.x - chunk * col_blocks;
@@ -1117,10 +1119,10 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
   // as the product.
   Decode dec = {};
   if (b.dW != nullptr && b.x == nullptr)
-    dec = Decode{b.x8, act8_rows(T, K), x_ws};  // T blocks <= 2^17 2^13: below 2^31
+    dec = Decode{b.x8, act8_rows(T, K), x_ws, act8_wide(x_ws, K)};  // T blocks <= 2^17 2^13: below 2^31
   const int col_blocks = (N + 255) / 256;
   const int dz_blocks = b.act != MF_ACT_NONE || b.db != nullptr ? chunks * col_blocks : 0;
-  const unsigned blocks = dz_blocks + act8_decode_blocks(dec.rows.items);
+  const unsigned blocks = dz_blocks + act8_ctas(dec.rows.items, dec.wide);
   if (blocks > 0) {
     float* p = b.db == nullptr ? nullptr : chunks > 1 ? part : b.db;
 #define MF_DZ(ACT, Z8)                                                                           \
