@@ -135,3 +135,26 @@ def test_other_stream_and_graph_replay():
     assert np.array_equal(q.cpu().numpy(), rq)
     v = oracle.act8_values(rq, rs)
     check_bf16(host(y), oracle.mlp_act(v, "silu"), np.abs(v) * (np.abs(v) + 8) * 2.0 ** -22, "replay")
+
+
+@pytest.mark.parametrize("C", [128, 264, 4096])
+def test_tensors_on_16_byte_boundaries(C):
+    """The least alignment the library asks for gives the same codes and values."""
+    T = 37
+    x = bf16(np.random.default_rng(C).standard_normal((T, C)))
+    q, s = _quantize(x)
+    y = torch.empty((T, C), dtype=torch.bfloat16, device="cuda")
+    mf.mf_act8_dequantize(q, s, T, C, mf.MF_ACT_GELU, y)
+
+    def off(n, dtype):
+        size = torch.empty(0, dtype=dtype).element_size()
+        v = torch.empty(n + 16, dtype=dtype, device="cuda")[16 // size:][:n]
+        assert v.data_ptr() % 32 == 16
+        return v
+
+    x2, q2 = off(T * C, torch.bfloat16).view(T, C), off(T * C, torch.int8).view(T, C)
+    s2, y2 = off(s.numel(), torch.float32).view(s.shape), off(T * C, torch.bfloat16).view(T, C)
+    x2.copy_(dev(x))
+    mf.mf_act8_quantize(x2, T, C, q2, s2)
+    mf.mf_act8_dequantize(q2, s2, T, C, mf.MF_ACT_GELU, y2)
+    assert torch.equal(q2, q) and torch.equal(s2, s) and torch.equal(y2, y)

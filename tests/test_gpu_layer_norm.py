@@ -220,3 +220,83 @@ def test_foreign_rows_do_not_leak():
                          T, 520, dx, dg, db, torch.empty(n, dtype=torch.uint8, device="cuda"), n)
     assert np.array_equal(host(dx)[mod == 0], clean[0][mod == 0])
     assert np.array_equal(host(dg)[0], clean[1][0]) and np.array_equal(host(db)[0], clean[2][0])
+
+
+def test_offsets_past_32_bits():
+    """2^31 + values: the last rows forward and backward, the sums theirs alone."""
+    hid = 8192
+    T = (1 << 31) // hid + 5
+    rng = np.random.default_rng(17)
+    tail, dtail = bf16(rng.standard_normal((6, hid))), bf16(rng.standard_normal((6, hid)))
+    gamma, beta = (np.float32(a + 0.1 * rng.standard_normal((2, hid))) for a in (1, 0))
+    mod = np.zeros(T, np.uint8)
+    mod[-3:] = 1
+    x = torch.zeros((T, hid), dtype=torch.bfloat16, device="cuda")
+    x[-6:] = dev(tail)
+    y = torch.empty_like(x)
+    st = torch.empty((T, 2), device="cuda")
+    tm = torch.from_numpy(mod).cuda()
+    mf.mf_layer_norm(x, dev32(gamma), dev32(beta), tm, T, hid, EPS, y, st)
+    ref, mean, rstd = oracle.layer_norm_affine(tail, gamma, beta, mod[-6:], EPS)
+    check_bf16(host(y[-6:]), ref, _norm_slack(tail, mean, rstd, gamma, beta, mod[-6:]), "tail")
+    y.zero_()
+    y[-6:] = dev(dtail)
+    dx = torch.empty_like(x)
+    dg, db = torch.empty((2, hid), device="cuda"), torch.empty((2, hid), device="cuda")
+    n = mf.mf_layer_norm_bwd_workspace_size(T, hid)
+    mf.mf_layer_norm_bwd(y, x, None, None, dev32(gamma), st, tm, None, T, hid, dx, dg, db,
+                         torch.empty(n, dtype=torch.uint8, device="cuda"), n)
+    assert mf.mf_get_error() == mf.MF_OK
+    s6 = host(st[-6:])
+    rdx, rdg, rdb = oracle.layer_norm_affine_bwd(dtail, tail, gamma, s6, mod[-6:])
+    # fp32 units of the row's terms as in test_backward, |xhat| <= 6, |g| <= 6 here
+    check_bf16(host(dx[-6:]), rdx, 2.0 ** -24 * 512 * np.abs(s6[:, 1:]), "dx tail")
+    np.testing.assert_allclose(host(dg), rdg, atol=16 * 2.0 ** -24 * 150)
+    np.testing.assert_allclose(host(db), rdb, atol=16 * 2.0 ** -24 * 30)
+    assert (dx[:-6] == 0).all()
+
+
+def test_tensors_on_16_byte_boundaries():
+    """The least alignment the library asks for."""
+    mod, x, gamma, beta, dy, resid = _data(MIXED, 1032, 23)
+    T, hid = x.shape
+
+    def off(t):
+        whole = torch.empty(t.numel() + 8, dtype=t.dtype, device="cuda")
+        v = whole[16 // t.element_size():][: t.numel()].view(t.shape)
+        v.copy_(t)
+        assert v.data_ptr() % 32 == 16
+        return v
+
+    want_y, want_st = _fwd(x, gamma, beta, mod)
+    y, st = off(torch.zeros((T, hid), dtype=torch.bfloat16)), torch.empty((T, 2), device="cuda")
+    tm = torch.from_numpy(mod).cuda()
+    mf.mf_layer_norm(off(dev(x)), off(dev32(gamma)), off(dev32(beta)), tm, T, hid, EPS, y, st)
+    assert np.array_equal(host(y), want_y) and np.array_equal(host(st), want_st)
+    want = _bwd(dy, x, gamma, want_st, mod, resid)
+    dx = off(torch.zeros((T, hid), dtype=torch.bfloat16))
+    dg, db = off(torch.zeros((2, hid))), off(torch.zeros((2, hid)))
+    n = mf.mf_layer_norm_bwd_workspace_size(T, hid)
+    mf.mf_layer_norm_bwd(off(dev(dy)), off(dev(x)), None, None, off(dev32(gamma)), st, tm,
+                         off(dev(resid)), T, hid, dx, dg, db,
+                         torch.empty(n, dtype=torch.uint8, device="cuda"), n)
+    for got, ref in zip((dx, dg, db), want):
+        assert np.array_equal(host(got), ref)
+
+
+def test_forward_replayed_on_another_stream():
+    mod, x, gamma, beta, _, _ = _data(MIXED, 768, 31)
+    T, hid = x.shape
+    other = bf16(x[::-1])
+    xt, y, st = dev(x), torch.empty((T, hid), dtype=torch.bfloat16, device="cuda"), torch.empty((T, 2), device="cuda")
+    args = [dev32(gamma), dev32(beta), torch.from_numpy(mod).cuda()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        mf.mf_layer_norm(xt, *args, T, hid, EPS, y, st)
+    xt.copy_(dev(other))
+    graph.replay()
+    torch.cuda.synchronize()
+    want_y, want_st = _fwd(other, gamma, beta, mod)
+    assert np.array_equal(host(y), want_y) and np.array_equal(host(st), want_st)

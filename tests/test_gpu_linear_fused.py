@@ -345,3 +345,66 @@ def test_offsets_past_32_bits():
     check_bf16(host(dx[-300:]), rdx, adx * (N + 2) * 2.0 ** -23, "dx")
     check_bf16(host(dW), rdW, adW * 400 * 2.0 ** -23, "dW")
     assert (np.abs(host(db) - rdb) <= 400 * 2.0 ** -24 * adb).all()
+
+
+@pytest.mark.parametrize("descs,K,N", [(MIXED, 256, 512), (((0, 0, 0, 40),), 256, 512)])
+def test_tensors_on_16_byte_boundaries(descs, K, N):
+    """The least alignment the library asks for gives the same bits."""
+    d = _data(descs, K, N, 51)
+    T = d["T"]
+    want = _fwd(descs, d, K, N, "gelu", keep=("bf16", "8bit"))
+    grads = _bwd(descs, d, K, N, "gelu", x8=True)
+
+    def off(t):
+        size = t.element_size()
+        v = torch.empty(t.numel() + 16, dtype=t.dtype, device="cuda")[16 // size:][: t.numel()].view(t.shape)
+        v.copy_(t)
+        assert v.data_ptr() % 32 == 16
+        return v
+
+    got = [off(torch.zeros_like(t)) for t in want]
+    tm = torch.from_numpy(d["mod"]).cuda()
+    W = off(dev(d["W"]))
+    mf.mf_linear_fused(off(dev(d["x"])), W, off(dev32(d["bias"])), off(dev(d["resid"])), tm, descs, K, N,
+                       mf.MF_ACT_GELU, got[1], got[2], got[3], got[0])
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    xq, xs, _ = _code(d["x"])
+    dx, dW, db = (off(torch.zeros_like(t)) for t in grads)
+    n = mf.mf_linear_fused_bwd_workspace_size(T, K, N)
+    mf.mf_linear_fused_bwd(off(dev(d["dout"])), None, off(xq), off(xs), W, off(dev(d["z"])), None, None, tm,
+                           descs, K, N, mf.MF_ACT_GELU, dx, dW, db,
+                           torch.empty(n, dtype=torch.uint8, device="cuda"), n)
+    for a, b in zip((dx, dW, db), grads):
+        assert torch.equal(a, b)
+
+
+def test_two_calls_in_a_row_into_the_same_buffers():
+    """The second call of a stream overwrites what the first wrote, few rows and many."""
+    for descs, K, N in ((((0, 0, 0, 24),), 512, 1024), (MIXED, 128, 264)):
+        a, b = _data(descs, K, N, 61), _data(descs, K, N, 62)
+        tm = torch.from_numpy(a["mod"]).cuda()
+        out = torch.empty((a["T"], N), dtype=torch.bfloat16, device="cuda")
+        xs = [dev(a["x"]), dev(b["x"])]
+        W = dev(a["W"])
+        want = torch.empty_like(out)
+        mf.mf_linear_fused(xs[1], W, None, None, tm, descs, K, N, 2, None, None, None, want)
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for x in xs:
+                mf.mf_linear_fused(x, W, None, None, tm, descs, K, N, 2, None, None, None, out)
+        assert torch.equal(out, want)
+
+
+def test_weight_sums_cut_over_the_tokens():
+    """A narrow layer over many tokens: the token axis in parts, joined in order."""
+    descs, K, N = ((1, 64, 80, 333), (1, 37, 41, 2001)), 72, 136
+    d = _data(descs, K, N, 71)
+    dx, dW, db = _bwd(descs, d, K, N, "none")
+    _, rdW, rdb, dz = oracle.linear_fused_bwd(d["dout"], d["x"], d["W"], None, d["mod"], "none")
+    _, adW, _, _ = oracle.linear_fused_bwd(np.abs(dz), np.abs(d["x"]), np.abs(d["W"]), None, d["mod"], "none")
+    check_bf16(host(dW), rdW, adW * (d["T"] + 64) * 2.0 ** -23, "dW")
+    mags = np.stack([np.abs(dz)[d["mod"] == m].sum(0) for m in (0, 1)])
+    assert (np.abs(host(db) - rdb) <= (d["T"] + 8) * 2.0 ** -24 * mags).all()
+    again = _bwd(descs, d, K, N, "none")
+    assert torch.equal(again[1], dW) and torch.equal(again[2], db)
