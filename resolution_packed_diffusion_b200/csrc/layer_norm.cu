@@ -23,9 +23,9 @@
 // one bulk copy per tensor brings them into a ring of shared-memory stages; the row
 // sums of g and g xhat are reduced by shuffles and, over several warps, at the one
 // barrier a step has, after which dx is formed from the same stage. The column sums
-// leave the registers when the modality changes and at the end, to the group's own
-// place, and a second kernel adds the CTAs' in a fixed order: no atomics, the same
-// bits every time.
+// leave the registers when the modality changes, to the group's own place, and at the
+// end; the CTAs of a cluster add theirs over distributed shared memory, and a second
+// kernel adds the clusters' in a fixed order: no atomics, the same bits every time.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -339,17 +339,20 @@ constexpr int kBwdRows = 2;  // rows per group and step: an even number, so that
 constexpr int kMaxStages = 4;
 
 // A thread owns CH chunks of eight channels, a.lanes chunks apart; FULL: all of them
-// exist (hid is 8 CH lanes), so nothing is guarded by the width. part:
-// [grid][2 modalities][2 (dgamma, dbeta)][hid], or dgamma and dbeta themselves when
-// the grid is one CTA (part NULL). Dynamic shared memory: the stages, then, with
-// more than one group, [groups][2][2][hid] fp32. One group adds into its place in
-// memory directly: each column has one owner.
+// exist (hid is 8 CH lanes), so nothing is guarded by the width. Dynamic shared
+// memory: the stages, then, with more than one group, the groups' places for sums of
+// a modality that ended, [groups][2 modalities][2 (dgamma, dbeta)][hid] fp32. A
+// single group's place is part[blockIdx.x][2][2][hid] in memory, and at the end its
+// totals stand in the stages' memory. sums_out[cluster][2][2][hid] (dgamma and dbeta
+// themselves where there is one cluster, sums_out NULL) gets the cluster's sums; a
+// cluster of several CTAs has one group in each.
 template <int SUB, int CH, int THREADS, int PER_SM, bool FULL, bool X8>
 __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
     const mf_bf16* __restrict__ dy, const mf_bf16* __restrict__ x, const Act8 x8,
     const float* __restrict__ gamma, const float2* __restrict__ stats, const mf_bf16* resid,
     const LnArgs a, const BwdStage sg, mf_bf16* dx, float* __restrict__ part,
-    float* __restrict__ dgamma, float* __restrict__ dbeta) {
+    float* __restrict__ sums_out, int cluster, float* __restrict__ dgamma,
+    float* __restrict__ dbeta) {
   constexpr int R = kBwdRows;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float red[2][32][2 * R];
@@ -412,16 +415,9 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
   int cm = -1, seen = 0;
   // this group's place for modality m: dgamma's row, dbeta's row
   auto place = [&](int m, float*& g, float*& b) {
-    if (a.groups > 1) {
-      g = cols + (static_cast<size_t>(group) * 4 + m * 2) * a.hid;
-      b = g + a.hid;
-    } else if (part != nullptr) {
-      g = part + (static_cast<size_t>(blockIdx.x) * 4 + m * 2) * a.hid;
-      b = g + a.hid;
-    } else {
-      g = dgamma + static_cast<size_t>(m) * a.hid;
-      b = dbeta + static_cast<size_t>(m) * a.hid;
-    }
+    g = (a.groups > 1 ? cols + static_cast<size_t>(group) * 4 * a.hid
+                      : part + static_cast<size_t>(blockIdx.x) * 4 * a.hid) + m * 2 * a.hid;
+    b = g + a.hid;
   };
   auto flush = [&]() {
     if (cm < 0) return;
@@ -616,32 +612,67 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
       parity ^= 1;
     }
   }
-  flush();
+  // The group's totals: what it put aside, and what it still holds.
+  __syncthreads();  // the stages are free
+  float* total = reinterpret_cast<float*>(smem);  // of a single group
+  float* mine = a.groups > 1 ? cols + static_cast<size_t>(group) * 4 * a.hid : total;
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {  // a modality that this group did not meet
-    if ((seen >> m) & 1) continue;
+  for (int m = 0; m < 2; ++m) {
     float *g, *b;
     place(m, g, b);
+    const bool more = (seen >> m) & 1, held = m == cm;
 #pragma unroll
-    for (int j = 0; j < CH; ++j)
-      if (on[j])
+    for (int j = 0; j < CH; ++j) {
+      if (!on[j]) continue;
+      const int c = (gl + j * a.lanes) * 8;
+      const uint64_t* g2 = reinterpret_cast<const uint64_t*>(g + c);
+      const uint64_t* b2 = reinterpret_cast<const uint64_t*>(b + c);
+      uint64_t* to_g = reinterpret_cast<uint64_t*>(mine + 2 * m * a.hid + c);
+      uint64_t* to_b = reinterpret_cast<uint64_t*>(mine + (2 * m + 1) * a.hid + c);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          g[(gl + j * a.lanes) * 8 + e] = b[(gl + j * a.lanes) * 8 + e] = 0.f;
-  }
-  if (a.groups == 1) return;
-  __syncthreads();
-  // the CTA's groups in order
-  for (int i = threadIdx.x; i < 4 * a.hid; i += blockDim.x) {
-    float v = 0.f;
-    for (int g = 0; g < a.groups; ++g) v += cols[static_cast<size_t>(g) * 4 * a.hid + i];
-    if (part != nullptr) {
-      part[static_cast<size_t>(blockIdx.x) * 4 * a.hid + i] = v;
-    } else {
-      const int m = i / (2 * a.hid), r = i - m * 2 * a.hid;
-      (r < a.hid ? dgamma : dbeta)[m * a.hid + (r < a.hid ? r : r - a.hid)] = v;
+      for (int e = 0; e < 4; ++e) {
+        uint64_t vg = held ? ag[j][e] : 0, vb = held ? ab[j][e] : 0;
+        if (more) {
+          vg = f2_add(g2[e], vg);
+          vb = f2_add(b2[e], vb);
+        }
+        to_g[e] = vg;
+        to_b[e] = vb;
+      }
     }
   }
+  // The CTA's groups in order, or the cluster's CTAs (a cluster's have one group each),
+  // four columns at a time; each CTA of a cluster adds every cluster-th four.
+  if (cluster > 1) cluster_sync();
+  else __syncthreads();
+  const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const float* first = a.groups > 1 ? cols : total;
+  for (int i = (threadIdx.x * cluster + rank) * 4; i < 4 * a.hid; i += blockDim.x * cluster * 4) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q = 0; q < (cluster > 1 ? cluster : a.groups); ++q) {
+      float4 w;
+      if (cluster > 1)
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(w.x), "=f"(w.y), "=f"(w.z), "=f"(w.w)
+                     : "r"(cluster_addr(first + i, q))
+                     : "memory");
+      else
+        w = *reinterpret_cast<const float4*>(first + static_cast<size_t>(q) * 4 * a.hid + i);
+      v.x += w.x;
+      v.y += w.y;
+      v.z += w.z;
+      v.w += w.w;
+    }
+    float* to;
+    if (sums_out != nullptr) {
+      to = sums_out + static_cast<size_t>(blockIdx.x / cluster) * 4 * a.hid + i;
+    } else {
+      const int m = i / (2 * a.hid), r = i - m * 2 * a.hid;
+      to = (r < a.hid ? dgamma : dbeta) + m * a.hid + (r < a.hid ? r : r - a.hid);
+    }
+    *reinterpret_cast<float4*>(to) = v;
+  }
+  if (cluster > 1) cluster_sync();  // no CTA leaves while another reads its totals
 }
 
 // dgamma / dbeta = the sum over the n partials, in a fixed order: 32 columns per
@@ -733,8 +764,15 @@ int bwd_grid(const RowShape& s, int32_t T) {
   const int steps = (T + s.groups * kBwdRows - 1) / (s.groups * kBwdRows), sms = ln_sms();
   if (steps <= sms) return steps;
   const int by_steps = steps / 4, cap = sms * bwd_per_sm(s);
-  return by_steps < sms ? sms : by_steps < cap ? by_steps : cap;
+  return (by_steps < sms ? sms : by_steps < cap ? by_steps : cap) / 2 * 2;
 }
+
+// CTAs that add their sums before they leave: pairs in wide rows, where that halves
+// what the second kernel reads (84 -> 78 us at 16384 x 3072, 38.2 -> 34.6 at 8464 x
+// 2048; 18.6 -> 19.8 at 4837 x 1000). Pairs all fit at once; clusters of four leave
+// SMs of a GPC out and come in two waves (117 us at 16384 x 3072).
+// Above 1024 channels a CTA has one group.
+int bwd_cluster(int grid, int32_t hid) { return hid > 1024 && grid % 2 == 0 ? 2 : 1; }
 
 template <int SUB, int CH, int THREADS, int PER_SM, bool FULL, bool X8>
 cudaError_t bwd_shape(const mf_bf16* dy, const mf_bf16* x, const Act8& x8, const float* gamma,
@@ -746,14 +784,29 @@ cudaError_t bwd_shape(const mf_bf16* dy, const mf_bf16* x, const Act8& x8, const
   const cudaError_t ae =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (ae != cudaSuccess) return ae;
-  const int grid = bwd_grid(s, a.T);
-  float* p = grid > 1 ? part : nullptr;
+  const int grid = bwd_grid(s, a.T), cluster = bwd_cluster(grid, a.hid);
+  const int clusters = grid / cluster;
+  float* sums = clusters > 1 ? part + static_cast<size_t>(grid) * 4 * a.hid : nullptr;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(s.threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   const cudaError_t e =
-      launch_dependent(kernel, dim3(grid), dim3(s.threads), smem, st, dy, x, x8, gamma,
-                       reinterpret_cast<const float2*>(stats), resid, a, g, dx, p, dgamma, dbeta);
-  if (e != cudaSuccess || p == nullptr) return e;
-  return launch_dependent(ln_cols_kernel, dim3((4 * a.hid + 31) / 32), dim3(1024), 0, st, p, grid,
-                          a.hid, dgamma, dbeta);
+      cudaLaunchKernelEx(&cfg, kernel, dy, x, x8, gamma, reinterpret_cast<const float2*>(stats),
+                         resid, a, g, dx, part, sums, cluster, dgamma, dbeta);
+  if (e != cudaSuccess || sums == nullptr) return e;
+  return launch_dependent(ln_cols_kernel, dim3((4 * a.hid + 31) / 32), dim3(1024), 0, st, sums,
+                          clusters, a.hid, dgamma, dbeta);
 }
 
 }  // namespace
@@ -775,7 +828,7 @@ cudaError_t launch_layer_norm(const mf_bf16* x, const float* gamma, const float*
 }
 
 size_t layer_norm_bwd_ws(int32_t T, int32_t hid) {
-  return static_cast<size_t>(bwd_grid(bwd_row_shape(hid), T)) * 4 * hid * sizeof(float);
+  return static_cast<size_t>(2 * bwd_grid(bwd_row_shape(hid), T)) * 4 * hid * sizeof(float);
 }
 
 cudaError_t launch_layer_norm_bwd(const mf_bf16* dy, const mf_bf16* x, const Act8& x8,
