@@ -717,12 +717,12 @@ template <int NCH>
 cudaError_t fwd_rows(const mf_bf16* x, const float* gamma, const float* beta, const LnArgs& a,
                      float eps, mf_bf16* y, float* stats, cudaStream_t st) {
   auto kernel = layer_norm_rows_kernel<NCH>;
+  // the limit of every width the instance takes: calls of two threads do not lower
+  // each other's
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NCH * 256 * 16);
+  if (e != cudaSuccess) return e;
   const int smem = a.hid * 16;
-  if (smem > 49152) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
   constexpr int kRowWarps = row_warps(NCH);
   const int need = (a.T + kRowWarps - 1) / kRowWarps, cap = ln_sms();
   return launch_dependent(kernel, dim3(need < cap ? need : cap), dim3(kRowWarps * 32), smem, st, x,
@@ -744,6 +744,8 @@ RowShape bwd_row_shape(int32_t hid) {
 // above 256 threads, whose registers leave no more room.
 int bwd_per_sm(const RowShape& s) { return s.threads > 256 ? 1 : 2; }
 
+constexpr int kBwdSmem = 222 * 1024;  // an SM's shared memory, the kernel's own 1 KB aside
+
 BwdStage bwd_stage(const RowShape& s, int32_t hid, bool x8, bool resid) {
   auto round128 = [](int v) { return (v + 127) / 128 * 128; };
   const int n = s.groups * kBwdRows * hid;
@@ -752,7 +754,7 @@ BwdStage bwd_stage(const RowShape& s, int32_t hid, bool x8, bool resid) {
   g.d = round128(2 * n);
   g.r = resid ? g.d : 0;
   const int cols = s.groups > 1 ? s.groups * 16 * hid : 0;
-  const int room = 222 * 1024 / bwd_per_sm(s) - 2048 - cols;
+  const int room = kBwdSmem / bwd_per_sm(s) - 2048 - cols;
   g.stages = room / g.bytes();
   if (g.stages > kMaxStages) g.stages = kMaxStages;
   return g;
@@ -782,7 +784,7 @@ cudaError_t bwd_shape(const mf_bf16* dy, const mf_bf16* x, const Act8& x8, const
   const BwdStage g = bwd_stage(s, a.hid, X8, resid != nullptr);
   const int smem = g.stages * g.bytes() + (s.groups > 1 ? s.groups * 16 * a.hid : 0);
   const cudaError_t ae =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
   if (ae != cudaSuccess) return ae;
   const int grid = bwd_grid(s, a.T), cluster = bwd_cluster(grid, a.hid);
   const int clusters = grid / cluster;

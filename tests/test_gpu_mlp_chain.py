@@ -104,3 +104,57 @@ def test_training_step_of_an_mlp_branch(descs, hid, F):
     for got, ref, name in ((dx, gdx, "dx"), (dW1, gdW1, "dW1"), (dW2, gdW2, "dW2"), (db1, gdb1, "db1"),
                            (db2, gdb2, "db2"), (dg, gdg, "dgamma"), (dbeta, gdbeta, "dbeta")):
         assert _rel(host(got), ref) < 0.023, name
+
+
+def test_captured_behind_copies_and_joined_streams():
+    """A capture in which the operators follow a memset, a copy and a join of two
+    streams, replayed on new inputs: every call waits for all that came before it."""
+    descs, hid, F = ((1, 9, 14, 5), (0, 0, 0, 133), (1, 14, 9, 2)), 256, 520
+    mod = modalities(descs)
+    T = len(mod)
+    rng = np.random.default_rng(3)
+    tm, arr = torch.from_numpy(mod).cuda(), mf.make_descs(descs)
+    gamma, beta = dev32(1 + 0.1 * rng.standard_normal((2, hid))), dev32(0.1 * rng.standard_normal((2, hid)))
+    W = dev(rng.standard_normal((2, F, hid)) / 16)
+    src = [dev(rng.standard_normal((T, hid))) for _ in range(2)]
+    inp, x, x1 = (torch.empty_like(src[0]) for _ in range(3))
+    q = torch.empty((T, hid), dtype=torch.int8, device="cuda")
+    s = torch.empty((T, 2), device="cuda")
+    h = torch.empty((T, F), dtype=torch.bfloat16, device="cuda")
+    bias = torch.empty((2, F), device="cuda")
+    dW = torch.empty_like(W)
+    n = mf.mf_linear_fused_bwd_workspace_size(T, hid, F)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step():
+        x.copy_(inp)                       # a copy before a call
+        mf.mf_layer_norm(x, gamma, beta, tm, T, hid, EPS, x1)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):      # a branch of its own
+            bias.zero_()
+            bias.add_(x1[0, 0].float())
+            mf.mf_act8_quantize(x1, T, hid, q, s)
+        mf.mf_linear_fused(x1, W, None, None, tm, arr, hid, F, mf.MF_ACT_SILU, None, None, None, h)
+        torch.cuda.current_stream().wait_stream(side)
+        mf.mf_linear_fused(x1, W, bias, None, tm, arr, hid, F, mf.MF_ACT_SILU, None, None, None, h)
+        mf.mf_linear_fused_bwd(h, None, q, s, None, None, None, None, tm, arr, hid, F, mf.MF_ACT_NONE,
+                               None, dW, None, ws, n)
+
+    want = []
+    with torch.cuda.stream(main):
+        for a in src:
+            inp.copy_(a)
+            step()
+            main.synchronize()
+            want.append([t.clone() for t in (x1, q, s, h, dW)])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            step()
+        for k in (0, 1, 1, 0):
+            inp.copy_(src[k])
+            graph.replay()
+            main.synchronize()
+            for got, ref in zip((x1, q, s, h, dW), want[k]):
+                assert torch.equal(got, ref)
+    assert mf.mf_get_error() == mf.MF_OK
