@@ -42,6 +42,7 @@
 
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "act8.cuh"
 #include "gemm_internal.h"
@@ -262,7 +263,8 @@ __device__ __forceinline__ Unit unit_of(const BwdArgs& a, int u) {
 // The walk over a dW unit's steps: run and first row of the current one.
 struct RunWalk {
   int r, row, left;
-  __device__ __forceinline__ void start(const BwdArgs& a, const Unit& w) {
+  template <class A>
+  __device__ __forceinline__ void start(const A& a, const Unit& w) {
     int lo = 0, hi = a.n[w.m] - 1;  // last run with it0 <= s0
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -273,7 +275,8 @@ struct RunWalk {
     row = a.start[w.m][r] + off;
     left = a.len[w.m][r] - off;
   }
-  __device__ __forceinline__ void next(const BwdArgs& a, int m) {
+  template <class A>
+  __device__ __forceinline__ void next(const A& a, int m) {
     row += kStepK;
     left -= kStepK;
     if (left <= 0 && r + 1 < a.n[m]) {
@@ -433,7 +436,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_uniform(static_cast<int>(threadIdx.x) >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i)
@@ -451,10 +454,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before either reaches the other's
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = warp_uniform(*tmem_slot);
   pdl_wait();
   pdl_release();
-  const int rank = static_cast<int>(cluster_ctarank());
+  const int rank = warp_uniform(static_cast<int>(cluster_ctarank()));
   const int unit0 = static_cast<int>(blockIdx.x >> 1);
   const int stride = static_cast<int>(gridDim.x >> 1);
 
@@ -533,58 +536,64 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      const uint32_t base = smem_u32(smem);
-      // a contiguous inner dimension: 16 elements are 32 bytes; a strided one: 16 rows
-      // of 128 bytes, the 64-column boxes kBoxBytes apart
-      const uint64_t a_flat = sdesc_sw128(base, 16, 1024);
-      const uint64_t a_rows = sdesc_sw128(base, kBoxBytes, 1024);
-      const uint64_t b_desc = sdesc_sw128(base + kABytes, MODE == kFwd ? 16 : kBoxBytes, 1024);
-      constexpr uint64_t B_STEP = MODE == kFwd ? 2 : 128;
+    // All lanes of the leader CTA's warp run the loop, lane 0 issues.
+    if (rank == 0) {
+      const bool leader = lane == 0;
+      const uint32_t base = warp_uniform(smem_u32(smem));
       uint32_t it = 0, ul = 0;
       bool ok = true;
-      for (int u = unit0; u < units && ok; u += stride, ++ul) {
-        const uint32_t acc = ul & 1;
-        if (!mbar_wait(&bars[kAccEmpty + acc], ((ul >> 1) & 1) ^ 1, args.ctl, abort_flag)) break;
-        tc_fence_after();
-        const Unit w = unit_of(args, u);
+      // A unit's steps; DW and B_MN say which way the operands run. A contiguous inner
+      // dimension: 16 elements are 32 bytes; a strided one: 16 rows of 128 bytes, the
+      // 64-column boxes kBoxBytes apart.
+      auto run = [&](auto dw, const Unit& w, uint32_t d, int width) {
+        constexpr bool DW = decltype(dw)::value, B_MN = MODE == kBwd;
+        constexpr uint64_t A_STEP = DW ? 128 : 2, B_STEP = B_MN ? 128 : 2;
+        const uint64_t a_desc = sdesc_sw128(base, DW ? kBoxBytes : 16, 1024);
+        const uint64_t b_desc = sdesc_sw128(base + kABytes, B_MN ? kBoxBytes : 16, 1024);
+        const uint32_t idesc = idesc_bf16_f32(2 * kHalf, width, DW, B_MN);
         RunWalk walk;
-        uint32_t idesc;
-        if constexpr (MODE == kFwd) {
-          idesc = idesc_bf16_f32(2 * kHalf, args.cols.width, 0, 0);
-        } else {
-          idesc = w.dw ? idesc_bf16_f32(2 * kHalf, args.dw_cols.width, 1, 1)
-                       : idesc_bf16_f32(2 * kHalf, args.dx_cols.width, 0, 1);
-          if (w.dw && w.steps > 0) walk.start(args, w);
-        }
-        const uint64_t a_desc = w.dw ? a_rows : a_flat;
-        const uint64_t a_step = w.dw ? 128 : 2;
-        const uint32_t d = tmem + acc * kTile;
+        if constexpr (DW)
+          if (w.steps > 0) walk.start(args, w);
         for (int s = 0; s < w.steps; ++s, ++it) {
           const int st = it % kStages;
           const uint32_t parity = (it / kStages) & 1;
           bool zeroed = false;  // rows zeroed by threads of both CTAs
-          if constexpr (MODE == kBwd)
-            if (w.dw) {
-              zeroed = walk.left < kStepK;
-              walk.next(args, w.m);
-            }
-          ok = zeroed ? mbar_wait_cluster(&bars[kFull + st], parity, args.ctl, abort_flag)
-                      : mbar_wait(&bars[kFull + st], parity, args.ctl, abort_flag);
-          if (!ok) break;
+          if constexpr (DW) {
+            zeroed = walk.left < kStepK;
+            walk.next(args, w.m);
+          }
+          ok = zeroed ? __all_sync(0xffffffffu, mbar_wait_cluster(&bars[kFull + st], parity,
+                                                                  args.ctl, abort_flag))
+                      : warp_wait(&bars[kFull + st], parity, args.ctl, abort_flag);
+          if (!ok) return;
           tc_fence_after();
           const uint64_t so = static_cast<uint64_t>((st * kStageBytes) >> 4);
 #pragma unroll
           for (int kk = 0; kk < kStepK / 16; ++kk)
-            umma_ss_pair(d, a_desc + so + kk * a_step, b_desc + so + kk * B_STEP, idesc,
-                         (s > 0 || kk > 0) ? 1u : 0u);
-          umma_commit_pair(&bars[kEmpty + st], 3);
+            umma_ss_pair_by(leader, d, a_desc + so + kk * A_STEP, b_desc + so + kk * B_STEP, idesc,
+                            (s > 0 || kk > 0) ? 1u : 0u);
+          umma_commit_pair_by(leader, &bars[kEmpty + st], 3);
+        }
+      };
+      for (int u = unit0; u < units && ok; u += stride, ++ul) {
+        const uint32_t acc = ul & 1;
+        if (!warp_wait(&bars[kAccEmpty + acc], ((ul >> 1) & 1) ^ 1, args.ctl, abort_flag)) break;
+        tc_fence_after();
+        const Unit w = unit_of(args, u);
+        const uint32_t d = tmem + acc * kTile;
+        if constexpr (MODE == kFwd) {
+          run(std::false_type{}, w, d, args.cols.width);
+        } else {
+          if (w.dw)
+            run(std::true_type{}, w, d, args.dw_cols.width);
+          else
+            run(std::false_type{}, w, d, args.dx_cols.width);
         }
         if (!ok) break;
-        umma_commit_pair(&bars[kAccFull + acc], 3);
+        umma_commit_pair_by(leader, &bars[kAccFull + acc], 3);
       }
       // every MMA this thread issued completes before TMEM is released
-      umma_commit_pair(&bars[kDrain], 1);
+      umma_commit_pair_by(leader, &bars[kDrain], 1);
       drain_wait(&bars[kDrain], 0, args.ctl.wait_limit_ns);
     }
     __syncwarp();

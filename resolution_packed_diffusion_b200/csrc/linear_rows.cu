@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) linear_rows_kernel(
   volatile int* abort_flag = &abort_word;
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_uniform(static_cast<int>(threadIdx.x) >> 5), lane = threadIdx.x & 31;
   const int stage_bytes = kWBytes + a.nt * kStepK * 2;
 
   if (threadIdx.x == 0) {
@@ -111,11 +111,11 @@ __global__ void __launch_bounds__(kThreads) linear_rows_kernel(
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = warp_uniform(tmem_slot);
   pdl_wait();
   pdl_release();
 
-  const int rank = static_cast<int>(cluster_ctarank());
+  const int rank = warp_uniform(static_cast<int>(cluster_ctarank()));
   const int unit = static_cast<int>(blockIdx.x) / a.splits;
   const int job = unit / a.tiles, out0 = (unit - job * a.tiles) * kOut;
   const int m = a.job_m[job];
@@ -145,28 +145,30 @@ __global__ void __launch_bounds__(kThreads) linear_rows_kernel(
     for (int i = 0; i < a.stages; ++i)
       if (issued > i)
         drain_wait(&full[i], ((issued - 1 - i) / a.stages) & 1, a.ctl.wait_limit_ns);
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
+    // all lanes run the loop, lane 0 issues
+    const bool leader = lane == 0;
     const uint32_t idesc = idesc_bf16_f32(kOut, a.nt, W_MN, 0);
     constexpr uint64_t W_STEP = W_MN ? 128 : 2;
-    const uint32_t base = smem_u32(smem);
+    const uint32_t base = warp_uniform(smem_u32(smem));
     int st = 0;
     uint32_t phase = 0;
     for (int s = s0; s < s1; ++s) {
-      if (!mbar_wait(&full[st], phase, a.ctl, abort_flag)) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[st], phase, a.ctl, abort_flag))) break;
       tc_fence_after();
       const uint32_t at = base + st * stage_bytes;
       const uint64_t dw = sdesc_sw128(at, W_MN ? kBoxBytes : 16, 1024);
       const uint64_t dx = sdesc_sw128(at + kWBytes, 16, 1024);
 #pragma unroll
       for (int kk = 0; kk < kStepK / 16; ++kk)
-        umma_ss(tmem, dw + kk * W_STEP, dx + kk * 2, idesc, (s > s0 || kk > 0) ? 1u : 0u);
-      umma_commit(&empty[st]);
+        umma_ss_by(leader, tmem, dw + kk * W_STEP, dx + kk * 2, idesc, (s > s0 || kk > 0) ? 1u : 0u);
+      umma_commit_by(leader, &empty[st]);
       if (++st == a.stages) {
         st = 0;
         phase ^= 1;
       }
     }
-    umma_commit(&done);
+    umma_commit_by(leader, &done);
   }
   __syncwarp();
   // A wait that ran out is recorded; the CTA still meets its cluster at the barriers.
