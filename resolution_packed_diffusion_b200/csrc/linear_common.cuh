@@ -61,6 +61,35 @@ __device__ __forceinline__ void umma_commit_pair_by(bool leader, uint64_t* bar, 
       : "memory");
 }
 
+// The producer's copies and byte counts in the same manner.
+__device__ __forceinline__ void load_2d_by(bool leader, void* dst, const CUtensorMap* map,
+                                           uint64_t* bar, int x, int y) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y),
+      "r"(static_cast<uint32_t>(leader))
+      : "memory");
+}
+__device__ __forceinline__ void load_2d_pair_by(bool leader, void* dst, const CUtensorMap* map,
+                                                uint32_t leader_bar, int x, int y) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(leader_bar), "r"(x), "r"(y),
+      "r"(static_cast<uint32_t>(leader))
+      : "memory");
+}
+__device__ __forceinline__ void expect_by(bool leader, uint64_t* bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(bytes), "r"(static_cast<uint32_t>(leader))
+      : "memory");
+}
+
 // L2 policy of the weights, which every row block reads again.
 __device__ __forceinline__ uint64_t keep_in_l2() {
   uint64_t p;

@@ -156,19 +156,24 @@ __device__ __forceinline__ void unit_coords(int u, int rows, int cols, int nb, i
 
 // Arrives on a barrier of either CTA of the pair and adds `bytes` to what it
 // expects.
-__device__ __forceinline__ void expect_pair(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
+__device__ __forceinline__ void expect_pair(bool leader, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes),
+      "r"(static_cast<uint32_t>(leader))
+      : "memory");
 }
 
 // A box of the weights: modality z of the (K, N, 2) map, completing on the
 // leader's barrier; kept in L2 (evict_last) since every row block reads it.
-__device__ __forceinline__ void load_w(void* dst, const CUtensorMap* map, uint32_t bar, int x,
-                                       int y, int z, uint64_t policy) {
+__device__ __forceinline__ void load_w(bool leader, void* dst, const CUtensorMap* map,
+                                       uint32_t bar, int x, int y, int z, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;\n\t}" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy),
+      "r"(static_cast<uint32_t>(leader))
       : "memory");
 }
 
@@ -462,81 +467,83 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int stride = static_cast<int>(gridDim.x >> 1);
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t keep = keep_in_l2();
-      uint32_t it = 0, part_uses = 0;  // bit st: parity of PART[st]'s uses
-      uint32_t part_used = 0;          // bit st: used at all
-      bool ok = true;
-      for (int u = unit0; u < units && ok; u += stride) {
-        const Unit w = unit_of(args, u);
-        RunWalk walk;
-        // this CTA's half of the tile's B columns; a strided B comes in boxes of 64
-        int width;
-        if constexpr (MODE == kFwd) {
-          width = args.cols.width;
-        } else {
-          width = w.dw ? args.dw_cols.width : args.dx_cols.width;
-          if (w.dw && w.steps > 0) walk.start(args, w);
-        }
-        const int half = width / 2;
-        const bool two = half > 64;
-        const uint32_t bytes =
-            kABytes + (MODE == kFwd ? half * kStepK * 2 : two ? 2 * kBoxBytes : kBoxBytes);
-        const int row = w.blk * kTile + rank * kHalf, col = w.ct * width + rank * half;
-        for (int s = 0; s < w.steps; ++s, ++it) {
-          const int st = it % kStages;
-          if (!(ok = mbar_wait(&bars[kEmpty + st], ((it / kStages) & 1) ^ 1, args.ctl, abort_flag)))
-            break;
-          uint8_t* sa = smem + st * kStageBytes;
-          uint8_t* sb = sa + kABytes;
-          if constexpr (MODE == kBwd) {
-            if (w.dw) {
-              if (walk.left < kStepK) {
-                uint64_t* bar = &bars[kPart + st];
-                mbar_expect_tx(bar, bytes);
-                tma_load_2d(sa, &map_c, bar, row, walk.row);
-                tma_load_2d(sa + kBoxBytes, &map_c, bar, row + 64, walk.row);
-                tma_load_2d(sb, &map_d, bar, col, walk.row);
-                if (two) tma_load_2d(sb + kBoxBytes, &map_d, bar, col + 64, walk.row);
-                part_uses ^= 1u << st;
-                part_used |= 1u << st;
-              } else {
-                const uint32_t bar = cluster_addr(&bars[kFull + st], 0);
-                expect_pair(bar, bytes);
-                tma_load_2d_pair(sa, &map_c, bar, row, walk.row);
-                tma_load_2d_pair(sa + kBoxBytes, &map_c, bar, row + 64, walk.row);
-                tma_load_2d_pair(sb, &map_d, bar, col, walk.row);
-                if (two) tma_load_2d_pair(sb + kBoxBytes, &map_d, bar, col + 64, walk.row);
-              }
-              walk.next(args, w.m);
-              continue;
+    // All lanes run the loop and lane 0 issues: with addresses and coordinates in uniform
+    // registers the copies of a step are out in time for 0.23 us a step, like the MMAs
+    // below (issued by one lane's branch: 0.29).
+    const bool leader = lane == 0;
+    const uint64_t keep = keep_in_l2();
+    uint32_t it = 0, part_uses = 0;  // bit st: parity of PART[st]'s uses
+    uint32_t part_used = 0;          // bit st: used at all
+    bool ok = true;
+    for (int u = unit0; u < units && ok; u += stride) {
+      const Unit w = unit_of(args, u);
+      RunWalk walk;
+      // this CTA's half of the tile's B columns; a strided B comes in boxes of 64
+      int width;
+      if constexpr (MODE == kFwd) {
+        width = args.cols.width;
+      } else {
+        width = w.dw ? args.dw_cols.width : args.dx_cols.width;
+        if (w.dw && w.steps > 0) walk.start(args, w);
+      }
+      const int half = width / 2;
+      const bool two = half > 64;
+      const uint32_t bytes =
+          kABytes + (MODE == kFwd ? half * kStepK * 2 : two ? 2 * kBoxBytes : kBoxBytes);
+      const int row = w.blk * kTile + rank * kHalf, col = w.ct * width + rank * half;
+      for (int s = 0; s < w.steps; ++s, ++it) {
+        const int st = it % kStages;
+        if (!(ok = warp_wait(&bars[kEmpty + st], ((it / kStages) & 1) ^ 1, args.ctl, abort_flag)))
+          break;
+        uint8_t* sa = smem + st * kStageBytes;
+        uint8_t* sb = sa + kABytes;
+        if constexpr (MODE == kBwd) {
+          if (w.dw) {
+            if (walk.left < kStepK) {
+              uint64_t* bar = &bars[kPart + st];
+              expect_by(leader, bar, bytes);
+              load_2d_by(leader, sa, &map_c, bar, row, walk.row);
+              load_2d_by(leader, sa + kBoxBytes, &map_c, bar, row + 64, walk.row);
+              load_2d_by(leader, sb, &map_d, bar, col, walk.row);
+              if (two) load_2d_by(leader, sb + kBoxBytes, &map_d, bar, col + 64, walk.row);
+              part_uses ^= 1u << st;
+              part_used |= 1u << st;
+            } else {
+              const uint32_t bar = cluster_addr(&bars[kFull + st], 0);
+              expect_pair(leader, bar, bytes);
+              load_2d_pair_by(leader, sa, &map_c, bar, row, walk.row);
+              load_2d_pair_by(leader, sa + kBoxBytes, &map_c, bar, row + 64, walk.row);
+              load_2d_pair_by(leader, sb, &map_d, bar, col, walk.row);
+              if (two) load_2d_pair_by(leader, sb + kBoxBytes, &map_d, bar, col + 64, walk.row);
             }
-          }
-          const uint32_t bar = cluster_addr(&bars[kFull + st], 0);
-          expect_pair(bar, bytes);
-          tma_load_2d_pair(sa, &map_a, bar, s * kStepK, row);
-          if constexpr (MODE == kFwd) {
-            load_w(sb, &map_b, bar, s * kStepK, col, w.m, keep);
-          } else {
-            load_w(sb, &map_b, bar, col, s * kStepK, w.m, keep);
-            if (two) load_w(sb + kBoxBytes, &map_b, bar, col + 64, s * kStepK, w.m, keep);
+            walk.next(args, w.m);
+            continue;
           }
         }
-      }
-      // Every copy lands before the CTA whose barrier it completes on can exit: the
-      // leader waits for both CTAs' on FULL, each CTA for its own on PART.
-      for (int st = 0; st < kStages; ++st) {
-        if (rank == 0 && it > static_cast<uint32_t>(st)) {
-          const uint32_t last = it - 1 - ((it - 1 - st) % kStages);
-          drain_wait(&bars[kFull + st], (last / kStages) & 1, args.ctl.wait_limit_ns);
+        const uint32_t bar = cluster_addr(&bars[kFull + st], 0);
+        expect_pair(leader, bar, bytes);
+        load_2d_pair_by(leader, sa, &map_a, bar, s * kStepK, row);
+        if constexpr (MODE == kFwd) {
+          load_w(leader, sb, &map_b, bar, s * kStepK, col, w.m, keep);
+        } else {
+          load_w(leader, sb, &map_b, bar, col, s * kStepK, w.m, keep);
+          if (two) load_w(leader, sb + kBoxBytes, &map_b, bar, col + 64, s * kStepK, w.m, keep);
         }
-        if ((part_used >> st) & 1)
-          drain_wait(&bars[kPart + st], ((part_uses >> st) & 1) ^ 1, args.ctl.wait_limit_ns);
       }
+    }
+    // Every copy lands before the CTA whose barrier it completes on can exit: the
+    // leader waits for both CTAs' on FULL, each CTA for its own on PART.
+    for (int st = 0; st < kStages; ++st) {
+      if (rank == 0 && it > static_cast<uint32_t>(st)) {
+        const uint32_t last = it - 1 - ((it - 1 - st) % kStages);
+        drain_wait(&bars[kFull + st], (last / kStages) & 1, args.ctl.wait_limit_ns);
+      }
+      if ((part_used >> st) & 1)
+        drain_wait(&bars[kPart + st], ((part_uses >> st) & 1) ^ 1, args.ctl.wait_limit_ns);
     }
     __syncwarp();
   } else if (warp == 1) {
-    // All lanes of the leader CTA's warp run the loop, lane 0 issues.
+    // The leader CTA's warp: all lanes run the loop, lane 0 issues.
     if (rank == 0) {
       const bool leader = lane == 0;
       const uint32_t base = warp_uniform(smem_u32(smem));

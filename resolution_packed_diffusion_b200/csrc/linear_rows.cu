@@ -49,12 +49,14 @@ struct RowsArgs {
   KernelCtl ctl;
 };
 
-__device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
-                                        int y, int z) {
+__device__ __forceinline__ void load_3d_by(bool leader, void* dst, const CUtensorMap* map,
+                                           uint64_t* bar, int x, int y, int z) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z),
+      "r"(static_cast<uint32_t>(leader))
       : "memory");
 }
 
@@ -121,21 +123,24 @@ __global__ void __launch_bounds__(kThreads) linear_rows_kernel(
   const int m = a.job_m[job];
   const int s0 = a.steps * rank / a.splits, s1 = a.steps * (rank + 1) / a.splits;
 
-  if (warp == 0 && lane == 0) {
+  // Both loops below are run by all lanes and issued from by lane 0, so that addresses
+  // and descriptors are in uniform registers.
+  const bool leader = lane == 0;
+  if (warp == 0) {
     int st = 0;
     uint32_t phase = 1;
     int issued = 0;
     for (int s = s0; s < s1; ++s, ++issued) {
-      if (!mbar_wait(&empty[st], phase, a.ctl, abort_flag)) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[st], phase, a.ctl, abort_flag))) break;
       uint8_t* sw = smem + st * stage_bytes;
-      mbar_expect_tx(&full[st], stage_bytes);
+      expect_by(leader, &full[st], stage_bytes);
       if constexpr (W_MN) {
-        load_3d(sw, &map_w, &full[st], out0, s * kStepK, m);
-        load_3d(sw + kBoxBytes, &map_w, &full[st], out0 + 64, s * kStepK, m);
+        load_3d_by(leader, sw, &map_w, &full[st], out0, s * kStepK, m);
+        load_3d_by(leader, sw + kBoxBytes, &map_w, &full[st], out0 + 64, s * kStepK, m);
       } else {
-        load_3d(sw, &map_w, &full[st], s * kStepK, out0, m);
+        load_3d_by(leader, sw, &map_w, &full[st], s * kStepK, out0, m);
       }
-      tma_load_2d(sw + kWBytes, &map_x, &full[st], s * kStepK, 0);
+      load_2d_by(leader, sw + kWBytes, &map_x, &full[st], s * kStepK, 0);
       if (++st == a.stages) {
         st = 0;
         phase ^= 1;
@@ -146,8 +151,6 @@ __global__ void __launch_bounds__(kThreads) linear_rows_kernel(
       if (issued > i)
         drain_wait(&full[i], ((issued - 1 - i) / a.stages) & 1, a.ctl.wait_limit_ns);
   } else if (warp == 1) {
-    // all lanes run the loop, lane 0 issues
-    const bool leader = lane == 0;
     const uint32_t idesc = idesc_bf16_f32(kOut, a.nt, W_MN, 0);
     constexpr uint64_t W_STEP = W_MN ? 128 : 2;
     const uint32_t base = warp_uniform(smem_u32(smem));
