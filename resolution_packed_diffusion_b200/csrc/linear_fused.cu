@@ -427,6 +427,23 @@ __device__ __forceinline__ void forward_row(const FwdArgs& a, uint32_t taddr, in
   }
 }
 
+// A pair's units, one of each round of `pairs`: in even rounds those of its own number
+// and in odd ones from the other end, so that with the longest units first the pairs
+// that had the longest get the shortest of what is left (dx and dW of 1000 -> 2056
+// over 2751 tokens: 51.3 -> 47.1 us), and a round begins with what is in L2 from the
+// one before (8464 x 12288 x 3072, with the decode of x: 1130 -> 1080 us).
+struct Queue {
+  int u, even, odd;
+  __device__ __forceinline__ Queue(int pair, int pairs)
+      : u(pair), even(2 * pairs - 1 - 2 * pair), odd(2 * pair + 1) {}
+  __device__ __forceinline__ void next() {
+    u += even;
+    const int t = even;
+    even = odd;
+    odd = t;
+  }
+};
+
 // Maps: forward x, W; backward dz and W for dx, dz and x for dW (map_c, map_d).
 template <int MODE>
 __global__ void __launch_bounds__(kWarps * 32, 1)
@@ -463,8 +480,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   pdl_wait();
   pdl_release();
   const int rank = warp_uniform(static_cast<int>(cluster_ctarank()));
-  const int unit0 = static_cast<int>(blockIdx.x >> 1);
-  const int stride = static_cast<int>(gridDim.x >> 1);
+  const Queue queue(static_cast<int>(blockIdx.x >> 1), static_cast<int>(gridDim.x >> 1));
 
   if (warp == 0) {
     // All lanes run the loop and lane 0 issues: with addresses and coordinates in uniform
@@ -475,8 +491,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     uint32_t it = 0, part_uses = 0;  // bit st: parity of PART[st]'s uses
     uint32_t part_used = 0;          // bit st: used at all
     bool ok = true;
-    for (int u = unit0; u < units && ok; u += stride) {
-      const Unit w = unit_of(args, u);
+    for (Queue q = queue; q.u < units && ok; q.next()) {
+      const Unit w = unit_of(args, q.u);
       RunWalk walk;
       // this CTA's half of the tile's B columns; a strided B comes in boxes of 64
       int width;
@@ -582,11 +598,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           umma_commit_pair_by(leader, &bars[kEmpty + st], 3);
         }
       };
-      for (int u = unit0; u < units && ok; u += stride, ++ul) {
+      for (Queue q = queue; q.u < units && ok; q.next(), ++ul) {
         const uint32_t acc = ul & 1;
         if (!warp_wait(&bars[kAccEmpty + acc], ((ul >> 1) & 1) ^ 1, args.ctl, abort_flag)) break;
         tc_fence_after();
-        const Unit w = unit_of(args, u);
+        const Unit w = unit_of(args, q.u);
         const uint32_t d = tmem + acc * kTile;
         if constexpr (MODE == kFwd) {
           run(std::false_type{}, w, d, args.cols.width);
@@ -613,10 +629,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const int cc0 = warp >= 8 ? kTile / 2 : 0;
     uint32_t ul = 0;
     bool stop = false;  // a wait ran out: the forward's warps still meet at their barrier
-    for (int u = unit0; u < units; u += stride, ++ul) {
+    for (Queue q = queue; q.u < units; q.next(), ++ul) {
       const uint32_t acc = ul & 1;
       const uint32_t taddr = tmem + lane_base + acc * kTile;
-      const Unit w = unit_of(args, u);
+      const Unit w = unit_of(args, q.u);
       const int r = w.blk * kTile + rank * kHalf + row;  // token, or row of dW
       if constexpr (MODE == kFwd) {
         const int n0 = w.ct * args.cols.width;
@@ -700,8 +716,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if constexpr (MODE == kBwd) {
       uint32_t it = 0, part_uses = 0;
       bool ok = true;
-      for (int u = unit0; u < units && ok; u += stride) {
-        const Unit w = unit_of(args, u);
+      for (Queue q = queue; q.u < units && ok; q.next()) {
+        const Unit w = unit_of(args, q.u);
         if (!w.dw) {
           it += w.steps;
           continue;
@@ -1018,20 +1034,30 @@ Columns columns(int cols, int width) {
 // Pairs of SMs on a B200 (148 SMs): what dW's split and its workspace are sized by.
 constexpr int kPairs = 74;
 
-// Column width of dW's tiles, by the tiles of one modality.
-int dw_width(int32_t K, int32_t N) { return tile_width(tiles_of(N), K, kPairs, 64); }
-int dw_tiles(int32_t K, int32_t N) {
-  const int w = dw_width(K, N);
-  return tiles_of(N) * ((K + w - 1) / w);
+// Tiles of one modality's dW at a column width.
+int dw_tiles(int32_t K, int32_t N, int width) {
+  return tiles_of(N) * ((K + width - 1) / width);
 }
 
-// Parts of a modality's steps: one, unless its tiles leave more than half of the
-// pairs without work; then as many as fill them, of at least 24 steps each (a step
-// takes about 0.35 us, joining the parts about 8 us).
+// Parts of a modality's steps: as many as fill the pairs, of at least kDwPartSteps
+// steps each, if that takes at least kDwJoinSteps steps off (a step takes about
+// 0.33 us, joining the parts about 8 us).
+constexpr int kDwPartSteps = 12, kDwJoinSteps = 24;
 int dw_splits(int tiles, int steps) {
-  const int by_pairs = kPairs / tiles, by_steps = steps / 24;
+  const int by_pairs = kPairs / tiles, by_steps = steps / kDwPartSteps;
   const int p = by_pairs < by_steps ? by_pairs : by_steps;
-  return p > 1 ? p : 1;
+  return p > 1 && steps - (steps + p - 1) / p >= kDwJoinSteps ? p : 1;
+}
+
+// Column width of dW's tiles: 256 if a modality's steps are split, and otherwise
+// narrower only while its tiles and the launch's others (`sets` modalities, `dx`) fit
+// one round.
+int dw_width(int32_t K, int32_t N, const int steps[2], int dx) {
+  int w = kTile;
+  const int tiles = dw_tiles(K, N, w), sets = (steps[0] > 0) + (steps[1] > 0);
+  if (dw_splits(tiles, steps[0]) > 1 || dw_splits(tiles, steps[1]) > 1) return w;
+  while (w > 64 && dx + sets * dw_tiles(K, N, w / 2) <= kPairs) w /= 2;
+  return w;
 }
 
 size_t round256(size_t v) { return (v + 255) / 256 * 256; }
@@ -1109,7 +1135,7 @@ cudaError_t launch_linear_fused(const mf_bf16* x, const mf_bf16* W, const TokenR
 // parts.
 size_t linear_fused_bwd_ws(int32_t T, int32_t K, int32_t N) {
   const size_t chunks = static_cast<size_t>((T + dz_rows(T) - 1) / dz_rows(T));
-  const size_t parts = dw_tiles(K, N) * 2 <= kPairs ? static_cast<size_t>(2) * kPairs : 0;
+  const size_t parts = dw_tiles(K, N, kTile) * 2 <= kPairs ? static_cast<size_t>(2) * kPairs : 0;
   return round256(static_cast<size_t>(T) * N * 2) + round256(chunks * 2 * N * sizeof(float)) +
          round256(static_cast<size_t>(T) * K * 2) + parts * kTile * kTile * sizeof(float);
 }
@@ -1185,14 +1211,11 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
       units[kDx] = a.jobs.n * a.dx_cols.tiles;
       cost[kDx] = static_cast<int64_t>((N + kStepK - 1) / kStepK) * a.dx_cols.width;
     }
-    const int dw_width_ = dw_width(K, N);
     int slots = 0;
     if (b.dW != nullptr) {
       if (!linear_map(&m[2], dz, N, T, 0, kStepK) ||
           !linear_map(&m[3], b.x != nullptr ? b.x : x_ws, K, T, 0, kStepK))
         return cudaErrorInvalidValue;
-      a.dw_cols = columns(K, dw_width_);
-      const int tiles = tiles_of(N) * a.dw_cols.tiles;
       for (int i = 0; i < 2; ++i) {
         a.n[i] = runs.n[i];
         a.it0[i][0] = 0;
@@ -1201,12 +1224,16 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
           a.len[i][r] = runs.len[i][r];
           a.it0[i][r + 1] = a.it0[i][r] + (runs.len[i][r] + kStepK - 1) / kStepK;
         }
-        const int steps = a.it0[i][runs.n[i]];
-        a.splits[i] = dw_splits(tiles, steps);
+      }
+      const int steps[2] = {a.it0[0][runs.n[0]], a.it0[1][runs.n[1]]};
+      a.dw_cols = columns(K, dw_width(K, N, steps, units[kDx]));
+      const int tiles = tiles_of(N) * a.dw_cols.tiles;
+      for (int i = 0; i < 2; ++i) {
+        a.splits[i] = dw_splits(tiles, steps[i]);
         a.slot0[i] = slots;
         units[kDwImage + i] = tiles * a.splits[i];
         if (a.splits[i] > 1) slots += units[kDwImage + i];
-        cost[kDwImage + i] = static_cast<int64_t>(steps / a.splits[i]) * dw_width_;
+        cost[kDwImage + i] = static_cast<int64_t>(steps[i] / a.splits[i]) * a.dw_cols.width;
       }
     }
     if (b.dx == nullptr || few_dx) m[0] = m[1] = m[2];

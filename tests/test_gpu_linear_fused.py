@@ -28,7 +28,13 @@ CASES = [(((0, 0, 0, 1),), 8, 8), (((1, 1, 1, 0),), 64, 256), (((1, 1, 1, 1),), 
          (((1, 3, 5, 2), (0, 0, 0, 7)), 1032, 392), (((1, 8, 8, 64),), 2048, 136),
          (((0, 0, 0, 33), (1, 3, 9, 1)), 4096, 1000), (((0, 0, 0, 1),), 4096, 2048),
          (((1, 2, 2, 4), (1, 1, 1, 1)), 328, 5128), (((1, 7, 17, 8),), 64, 1024),
-         (((0, 0, 0, 129),), 512, 256)]
+         (((0, 0, 0, 129),), 512, 256),
+         # dW's tokens in parts: of one modality, of both, of many runs; dW in narrow
+         # tiles beside dx's
+         (((1, 47, 55, 3), (0, 0, 0, 5)), 264, 520),
+         (((1, 37, 53, 1901), (1, 11, 13, 77)), 200, 328),
+         (tuple((1, 7, 9, 31) for _ in range(40)), 520, 264),
+         (((1, 25, 40, 300),), 136, 72)]
 
 
 def _data(descs, K, N, seed):
