@@ -29,9 +29,9 @@
 // operands, between the copies and the MMAs, so that an infinity or NaN in a
 // foreign row has no effect. Whole steps go from the copies to the MMAs directly:
 // sending every step through a warp that hands it on across the pair cost 1.0 us a
-// step, against 0.45 us for its copies and MMAs.
-//   warp 0      TMA producer (one lane)
-//   warp 1      tcgen05 issuer (one lane of the leader CTA)
+// step, against 0.33 us for its copies and MMAs with every pair at work (0.22 alone).
+//   warp 0      TMA producer (all lanes in the loop, one issues)
+//   warp 1      tcgen05 issuer (likewise, in the leader CTA)
 //   warp 2      backward: zeroes the rows past a run
 //   warp 3      backward: adds the partial sums of db that dz_kernel left
 //   warps 4..11 epilogue, from the accumulator that the MMAs have left for the other
@@ -429,9 +429,8 @@ __device__ __forceinline__ void forward_row(const FwdArgs& a, uint32_t taddr, in
 
 // A pair's units, one of each round of `pairs`: in even rounds those of its own number
 // and in odd ones from the other end, so that with the longest units first the pairs
-// that had the longest get the shortest of what is left (dx and dW of 1000 -> 2056
-// over 2751 tokens: 51.3 -> 47.1 us), and a round begins with what is in L2 from the
-// one before (8464 x 12288 x 3072, with the decode of x: 1130 -> 1080 us).
+// that had the longest get the shortest of what is left (dz, dx and dW of 1000 -> 2056
+// over 2751 tokens: 51.3 -> 47.1 us; no difference where there are many rounds).
 struct Queue {
   int u, even, odd;
   __device__ __forceinline__ Queue(int pair, int pairs)
@@ -484,7 +483,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
   if (warp == 0) {
     // All lanes run the loop and lane 0 issues: with addresses and coordinates in uniform
-    // registers the copies of a step are out in time for 0.23 us a step, like the MMAs
+    // registers the copies of a step are out in time for 0.22 us a step, like the MMAs
     // below (issued by one lane's branch: 0.29).
     const bool leader = lane == 0;
     const uint64_t keep = keep_in_l2();
@@ -1006,10 +1005,11 @@ int tile_width(int rows, int cols, int pairs, int least) {
 
 // The forward's, in two or three rounds: the width whose rounds cost least, a round
 // as much as its width and 200 columns more (1000 -> 2056 over 2751 tokens: 208
-// columns, 30.2 us against 32.9). Beyond that 256 is best whatever the last round
-// holds (8464 x 3072 x 12288: 240 columns would be 22.5 rounds' worth in place of 23
-// and take 502 us in place of 483), and dx, whose B operand comes in 64-column boxes,
-// gains nothing from other widths (33.8 us at 240 against 30.9, 4096 -> 1024 over 2464).
+// columns, 22.2 us against 24.0; 1024 -> 4096 over 2464: 192, 24.1 against 26.2).
+// Beyond that 256 is best whatever the last round holds (8464 x 3072 x 12288: 240
+// columns would be 22.5 rounds' worth in place of 23 and take 429 us in place of 421),
+// and dx, whose B operand comes in 64-column boxes, loses at widths between them
+// (4096 -> 1024 over 2464: 30.8 us at 240 against 27.9).
 int forward_width(int rows, int cols, int pairs, bool blocks) {
   const int w = tile_width(rows, cols, pairs, blocks ? kAct8Block : 64);
   if (w < kTile || blocks || pairs <= 0) return w;
@@ -1040,8 +1040,9 @@ int dw_tiles(int32_t K, int32_t N, int width) {
 }
 
 // Parts of a modality's steps: as many as fill the pairs, of at least kDwPartSteps
-// steps each, if that takes at least kDwJoinSteps steps off (a step takes about
-// 0.33 us, joining the parts about 8 us).
+// steps each, if that takes at least kDwJoinSteps steps off: a step takes about
+// 0.33 us, joining the parts about 8 us (dx and dW, 256 -> 1024 over 4160 tokens: 20.4
+// us in 2 parts, 16.0 in 5; 1000 -> 2056 over 2751: 43.2 in 2 parts, 40.2 whole).
 constexpr int kDwPartSteps = 12, kDwJoinSteps = 24;
 int dw_splits(int tiles, int steps) {
   const int by_pairs = kPairs / tiles, by_steps = steps / kDwPartSteps;
@@ -1051,7 +1052,9 @@ int dw_splits(int tiles, int steps) {
 
 // Column width of dW's tiles: 256 if a modality's steps are split, and otherwise
 // narrower only while its tiles and the launch's others (`sets` modalities, `dx`) fit
-// one round.
+// one round: a step takes as long at any width, so narrow tiles in several rounds lose
+// (dx and dW, 512 -> 2048 over 8464 tokens: 57.2 us at 64 columns, 36.4 at 256 in
+// parts; 1000 -> 1000 over 3912: 37.5 and 31.8).
 int dw_width(int32_t K, int32_t N, const int steps[2], int dx) {
   int w = kTile;
   const int tiles = dw_tiles(K, N, w), sets = (steps[0] > 0) + (steps[1] > 0);
