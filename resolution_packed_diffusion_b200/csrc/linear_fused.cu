@@ -313,13 +313,42 @@ __device__ __forceinline__ void add_bias32(const float* bias, float (&f)[32]) {
   }
 }
 
-// 32 columns of a residual row, as far as they exist.
+// A thread moves runs of its own row, so a warp's access touches 32 rows: with 32 bytes
+// a thread it moves whole sectors; with 16, half of each twice. Rows that begin in the
+// middle of a sector are moved as 16, 32 and 16 bytes (2751 x 1000 x 2056 with a
+// residual and z: 29.0 us as four times 16, 28.3 so).
+__device__ __forceinline__ void store_sector8(void* p, const uint32_t (&r)[8]) {
+  store_sector(p, make_uint4(r[0], r[1], r[2], r[3]), make_uint4(r[4], r[5], r[6], r[7]));
+}
+__device__ __forceinline__ bool sector_aligned(const void* p) {
+  return (reinterpret_cast<uintptr_t>(p) & 31u) == 0;
+}
+
+// 32 columns of a residual row, as far as they exist (`left`, a multiple of 8).
 struct Resid32 {
   uint4 v[4];
+  template <int Q>
+  __device__ __forceinline__ void one(const mf_bf16* p, int left) {
+    if (left > 8 * Q) v[Q] = *(reinterpret_cast<const uint4*>(p) + Q);
+  }
+  template <int Q>
+  __device__ __forceinline__ void two(const mf_bf16* p, int left) {
+    if (left > 8 * Q + 8)
+      load_sector(p + 8 * Q, v[Q], v[Q + 1]);
+    else
+      one<Q>(p, left);
+  }
   __device__ __forceinline__ void load(const mf_bf16* p, int left) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      v[q] = q * 8 < left ? *(reinterpret_cast<const uint4*>(p) + q) : make_uint4(0, 0, 0, 0);
+    for (int q = 0; q < 4; ++q) v[q] = make_uint4(0, 0, 0, 0);
+    if (sector_aligned(p)) {
+      two<0>(p, left);
+      two<2>(p, left);
+    } else {
+      one<0>(p, left);
+      two<1>(p, left);
+      one<3>(p, left);
+    }
   }
   __device__ __forceinline__ void add(float (&f)[32]) const {
 #pragma unroll
@@ -332,31 +361,29 @@ struct Resid32 {
   }
 };
 
-// A thread stores runs of its own row, so a warp's store touches 32 rows: with 32
-// bytes a thread it writes whole sectors; with 16 it would write half of each, twice.
-__device__ __forceinline__ void store_sector8(void* p, const uint32_t (&r)[8]) {
-  store_sector(p, make_uint4(r[0], r[1], r[2], r[3]), make_uint4(r[4], r[5], r[6], r[7]));
-}
-__device__ __forceinline__ bool sector_aligned(const void* p) {
-  return (reinterpret_cast<uintptr_t>(p) & 31u) == 0;
-}
-
 // Up to 32 columns (`left`, a multiple of 8) in bf16.
 __device__ __forceinline__ void store32(mf_bf16* p, int left, const float (&f)[32]) {
-  const bool wide = sector_aligned(p);
+  uint4 v[4];
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    uint32_t r[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = pack_bf16x2(f[16 * q + 2 * e], f[16 * q + 2 * e + 1]);
-    if (wide && left >= 16 * (q + 1)) {
-      store_sector8(p + 16 * q, r);
-    } else {
-      if (left > 16 * q)
-        __stcs(reinterpret_cast<uint4*>(p + 16 * q), make_uint4(r[0], r[1], r[2], r[3]));
-      if (left > 16 * q + 8)
-        __stcs(reinterpret_cast<uint4*>(p + 16 * q + 8), make_uint4(r[4], r[5], r[6], r[7]));
-    }
+  for (int q = 0; q < 4; ++q)
+    v[q] = make_uint4(pack_bf16x2(f[8 * q], f[8 * q + 1]), pack_bf16x2(f[8 * q + 2], f[8 * q + 3]),
+                      pack_bf16x2(f[8 * q + 4], f[8 * q + 5]), pack_bf16x2(f[8 * q + 6], f[8 * q + 7]));
+  auto one = [&](int q) {
+    if (left > 8 * q) __stcs(reinterpret_cast<uint4*>(p) + q, v[q]);
+  };
+  auto two = [&](int q) {
+    if (left > 8 * q + 8)
+      store_sector(p + 8 * q, v[q], v[q + 1]);
+    else
+      one(q);
+  };
+  if (sector_aligned(p)) {
+    two(0);
+    two(2);
+  } else {
+    one(0);
+    two(1);
+    one(3);
   }
 }
 
