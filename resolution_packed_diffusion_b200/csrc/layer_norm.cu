@@ -31,6 +31,7 @@
 #include <cstdint>
 
 #include "act8.cuh"
+#include "linear_common.cuh"
 #include "mlp_internal.h"
 #include "pdl.cuh"
 
@@ -404,8 +405,9 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
     bulk_load(dst + sg.x, dy + off, 2 * n, bar);
     if (resid != nullptr) bulk_load(dst + sg.x + sg.d, resid + off, 2 * n, bar);
   };
+  int issued = 0;  // thread 0: steps whose copies it has started
   if (threadIdx.x == 0)
-    for (int s = 0; s < sg.stages && s < steps; ++s) issue(s, s);
+    for (; issued < sg.stages && issued < steps; ++issued) issue(issued, issued);
 
   uint64_t gam[CH][4], ag[CH][4], ab[CH][4];
 #pragma unroll
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
     const uint8_t* sr = sd + sg.d;
     sx += X8 ? elem : 2 * elem;
     // A wait that runs out is recorded and the step goes on, so that every thread
-    // still meets every barrier.
+    // still meets every barrier; no copy is started after it.
     (void)mbar_wait(&full[at], parity, a.ctl, abort_flag);
     auto operands = [&](int i, int j, uint64_t (&h)[4], uint64_t (&d)[4]) {
       const uint32_t o = i * a.hid + j * chunk;
@@ -566,7 +568,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
     if (SUB == 32 && warps > 1 && lane < 4) red[s & 1][threadIdx.x >> 5][lane] = part4;
     __syncthreads();
     // every thread has left the previous step, so its stage can be filled again
-    if (threadIdx.x == 0 && s > 0 && s - 1 + sg.stages < steps) issue(s - 1 + sg.stages, prev);
+    if (threadIdx.x == 0 && s > 0 && issued < steps && !*abort_flag) issue(issued++, prev);
     if (SUB == 32 && warps > 1) {
       // sum l mod 4 of the group's warps, eight of them at a time
       part4 = 0.f;
@@ -612,6 +614,11 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
       parity ^= 1;
     }
   }
+  // After a wait that ran out the last copies may still be under way; otherwise every
+  // one has been waited for.
+  if (threadIdx.x == 0 && *abort_flag)
+    for (int s = max(0, issued - sg.stages); s < issued; ++s)
+      drain_wait(&full[s % sg.stages], (s / sg.stages) & 1, a.ctl.wait_limit_ns);
   // The group's totals: what it put aside, and what it still holds.
   __syncthreads();  // the stages are free
   float* total = reinterpret_cast<float*>(smem);  // of a single group

@@ -300,3 +300,37 @@ def test_forward_replayed_on_another_stream():
     torch.cuda.synchronize()
     want_y, want_st = _fwd(other, gamma, beta, mod)
     assert np.array_equal(host(y), want_y) and np.array_equal(host(st), want_st)
+
+
+@pytest.mark.parametrize("hid,ckpt", [(264, False), (1536, False), (3000, True)])
+def test_a_backward_whose_waits_run_out_leaves_nothing_behind(hid, ckpt):
+    """With a limit of 1 ns a wait for the first copies may run out: the call then
+    reports it, having started no further copies and waited for those under way, and
+    the next call under the usual limit is as good as ever."""
+    descs = ((1, 40, 41, 60), (1, 30, 7, 900))
+    mod, x, gamma, beta, dy, resid = _data(descs, hid, 61)
+    xv = oracle.act8_values(*oracle.act8_quantize(x)) if ckpt else x
+    _, mean, rstd = oracle.layer_norm_affine(xv, gamma, beta, mod, EPS)
+    st = np.float32(np.stack([mean, rstd], 1))
+    want = _bwd(dy, x, gamma, st, mod, resid, ckpt=ckpt)
+    T = len(mod)
+    x8, xs = (torch.from_numpy(a).cuda() for a in oracle.act8_quantize(x))
+    n = mf.mf_layer_norm_bwd_workspace_size(T, hid)
+    args = [dev(dy), *((None, x8, xs) if ckpt else (dev(x), None, None)), dev32(gamma), dev32(st),
+            torch.from_numpy(mod).cuda(), dev(resid), T, hid]
+    dx, dxc = guarded((T, hid), torch.bfloat16)
+    out = [dx, torch.empty((2, hid), device="cuda"), torch.empty((2, hid), device="cuda"),
+           torch.empty(n, dtype=torch.uint8, device="cuda"), n]
+    try:
+        mf.mf_set_wait_limit_ns(1)
+        for _ in range(4):
+            mf.mf_layer_norm_bwd(*args, *out)
+            status = mf.mf_get_error()
+            assert status in (mf.MF_OK, mf.MF_ERR_TIMEOUT)
+            if status == mf.MF_OK:
+                assert np.array_equal(host(dx), want[0])
+            dxc()
+    finally:
+        mf.mf_set_wait_limit_ns(2_000_000_000)
+    for got, ref in zip(_bwd(dy, x, gamma, st, mod, resid, ckpt=ckpt), want):
+        assert np.array_equal(got, ref)
