@@ -95,6 +95,29 @@ def test_forward_every_row(k):
             np.stack(tol, 1) + 2.0 ** -22 * np.stack(blocks, 1)).all()
 
 
+# Widths of the column tiles from 144 to 240, and 256 in four rounds, over a pack whose row
+# blocks hold both modalities (14 jobs for the 74 pairs of SMs): (K, N, columns of a tile)
+WIDTHS = [(72, 1328, 144), (136, 1488, 160), (64, 2640, 176), (200, 2648, 192), (1000, 2056, 208),
+          (136, 3128, 224), (520, 1128, 240), (40, 3848, 256)]
+
+
+@pytest.mark.parametrize("keep", [(), ("bf16",)], ids=["out", "z"])
+@pytest.mark.parametrize("k", range(len(WIDTHS)))
+def test_forward_column_widths(k, keep):
+    """One to four rounds of tiles whose width is no power of two: bias, residual and
+    every row, with and without the pre-activation."""
+    descs, (K, N, _) = ((1, 31, 33, 7), (1, 17, 91, 45), (0, 0, 0, 129)), WIDTHS[k]
+    d = _data(descs, K, N, 200 + k)
+    act = ("silu", "none", "gelu")[k % 3]
+    out, z, _, _ = _fwd(descs, d, K, N, act, keep=keep, in_place=k % 2 == 1)
+    ref, rz = oracle.linear_fused(d["x"], d["W"], d["bias"], d["resid"], d["mod"], act)
+    slack = _sum_slack(d["x"], d["W"], d["mod"], K) + 2.0 ** -23 * np.abs(rz)
+    aslack = 1.13 * slack + np.abs(rz) * (np.abs(rz) * (1.6 + 0.0714 * rz * rz) + 8) * 2.0 ** -22
+    check_bf16(host(out), ref, aslack + 2.0 ** -23 * np.abs(ref), "out")
+    if keep:
+        check_bf16(host(z), rz, slack, "z")
+
+
 def test_forward_variants_agree():
     """What is kept beside the output does not change it, and calls repeat bit for bit."""
     descs, K, N = MIXED, 192, 392
