@@ -158,3 +158,16 @@ def test_tensors_on_16_byte_boundaries(C):
     mf.mf_act8_quantize(x2, T, C, q2, s2)
     mf.mf_act8_dequantize(q2, s2, T, C, mf.MF_ACT_GELU, y2)
     assert torch.equal(q2, q) and torch.equal(s2, s) and torch.equal(y2, y)
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_a_nan_block_ends_where_it_ends(act):
+    """The block beside one that reads back as NaN is as it would be."""
+    rng = np.random.default_rng(29)
+    x = bf16(rng.standard_normal((5, 392)))
+    q, s = oracle.act8_quantize(x)
+    s[2, 1] = np.nan
+    y = torch.empty((5, 392), dtype=torch.bfloat16, device="cuda")
+    mf.mf_act8_dequantize(torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda(), 5, 392, ACTS[act], y)
+    bad = torch.isnan(y.float()).cpu().numpy()
+    assert bad[2, 128:256].all() and bad.sum() == 128

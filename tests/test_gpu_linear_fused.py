@@ -437,3 +437,55 @@ def test_weight_sums_cut_over_the_tokens():
     assert (np.abs(host(db) - rdb) <= (d["T"] + 8) * 2.0 ** -24 * mags).all()
     again = _bwd(descs, d, K, N, "none")
     assert torch.equal(again[1], dW) and torch.equal(again[2], db)
+
+
+NAN_PACKS = {"few rows": ((1, 3, 5, 2), (0, 0, 0, 23)), "many rows": MIXED}
+
+
+@pytest.mark.parametrize("n0", [6, 133])
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("pack", list(NAN_PACKS))
+def test_a_nan_channel_stays_alone(pack, act, n0):
+    """A NaN in one channel's bias, weights or pre-activation: every other channel, the
+    one beside it too, as it would be."""
+    descs, K, N = NAN_PACKS[pack], 72, 264
+    d = _data(descs, K, N, 81)
+    T, mod = d["T"], d["mod"]
+    others = np.arange(N) != n0
+    ref, rz = oracle.linear_fused(d["x"], d["W"], d["bias"], d["resid"], mod, act)
+    slack = _sum_slack(d["x"], d["W"], mod, K) + 2.0 ** -23 * np.abs(rz)
+    aslack = 1.13 * slack + np.abs(rz) * (np.abs(rz) * (1.6 + 0.0714 * rz * rz) + 8) * 2.0 ** -22
+    aslack += 2.0 ** -23 * np.abs(ref)
+    text, tm = mod == 1, torch.from_numpy(mod).cuda()
+    for where in ("bias", "weights"):
+        W, bias = dev(d["W"]), dev32(d["bias"])
+        if where == "bias":
+            bias[1, n0] = float("nan")
+        else:
+            W[1, n0, 3] = float("nan")
+        out, z = (torch.empty((T, N), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        mf.mf_linear_fused(dev(d["x"]), W, bias, dev(d["resid"]), tm, descs, K, N, ACTS[act], z, None, None, out)
+        got = host(out)
+        assert np.isnan(got[text, n0]).all() and np.isnan(host(z)[text, n0]).all(), where
+        check_bf16(got[:, others], ref[:, others], aslack[:, others], f"out, {where}")
+        check_bf16(got[~text, n0], ref[~text, n0], aslack[~text, n0], f"image rows, {where}")
+
+    # backward: one NaN pre-activation in a text row
+    t0 = int(np.flatnonzero(text)[-1])
+    rdx, rdW, rdb, dz = oracle.linear_fused_bwd(d["dout"], d["x"], d["W"], d["z"], mod, act)
+    zt = dev(d["z"])
+    zt[t0, n0] = float("nan")
+    dx, dW, db = (host(t) for t in _bwd(descs, d, K, N, act, z=zt))
+    assert np.isnan(dx[t0]).all() and np.isnan(dW[1, n0]).all() and np.isnan(db[1, n0])
+    w = np.abs(d["z"]) * (1.6 + 0.0714 * d["z"] ** 2)
+    dz_slack = np.abs(d["dout"]) * (2 + w) * (w + 8) * 2.0 ** -22
+    adz = np.abs(dz) + dz_slack
+    adx, adW, adb, _ = oracle.linear_fused_bwd(adz, np.abs(d["x"]), np.abs(d["W"]), None, mod, "none")
+    sdx, sdW, sdb, _ = oracle.linear_fused_bwd(dz_slack, np.abs(d["x"]), np.abs(d["W"]), None, mod, "none")
+    rows = np.arange(T) != t0
+    check_bf16(dx[rows], rdx[rows], (adx * (2.0 ** -8 + (N + 2) * 2.0 ** -23) + sdx)[rows], "dx")
+    tol = adW * (2.0 ** -8 + (T + 64) * 2.0 ** -23) + sdW
+    check_bf16(dW[0], rdW[0], tol[0], "dW of the image")
+    check_bf16(dW[1, others], rdW[1, others], tol[1, others], "dW of the text")
+    tol = (T + 8) * 2.0 ** -24 * adb + sdb
+    assert (np.abs(db - rdb)[0] <= tol[0]).all() and (np.abs(db - rdb)[1, others] <= tol[1, others]).all()
