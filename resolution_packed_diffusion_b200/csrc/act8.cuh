@@ -125,15 +125,17 @@ __device__ __forceinline__ float rcp_approx(float x) {
 
 // act(z) and act'(z) of pairs. GELU, tanh form: 0.5 z (1 + tanh u) = z sigma(2u) with
 // u = sqrt(2/pi) (z + 0.044715 z^3); SiLU: z sigma(z). Both are z sigma(w), w = c1 z +
-// c3 z^3, so act' = sigma + z sigma (1 - sigma) w'. sigma(w) = 1 / (1 + 2^v), v = -w
-// log2(e); a pair shares one reciprocal, 1 / ((1 + a)(1 + b)), since two special
-// functions a value already bound these kernels. z is held at ActCoef::low, where act and
-// act' are below 1e-16 in magnitude, so that the product cannot overflow (2^v < 2^62);
-// act' holds it at 30 too, where sigma is 1. A NaN stays in its own lane: the shared
-// reciprocal sees 2^62 in its place (a minimum with a number drops NaN), and the product
-// with z makes that lane's result NaN again. BLOCK: values read back from a checkpoint,
-// whose blocks are NaN throughout or not at all, go without the minimum (16384 x 12288
-// stored and read back through the GELU: 204.2 us, 207.8 with it).
+// c3 z^3, so act' = sigma + z w' sigma (1 - sigma). sigma(w) = 1 / (1 + e), e = 2^v, v =
+// -w log2(e); a pair shares one reciprocal, 1 / ((1 + a)(1 + b)), since two special
+// functions a value already bound these kernels. 1 - sigma is taken as e sigma: where
+// sigma is near 1, sigma - sigma^2 is the reciprocal's rounding and no more, and z w' of
+// GELU, up to 5800, made it 7e-4 (measured). z is held at ActCoef::low, where act and act' are
+// below 1e-16 in magnitude, so that the product cannot overflow (e < 2^62); act' holds it
+// at 30 too, where e is 0. A NaN stays in its own lane: the shared reciprocal sees 2^62 in
+// its place (a minimum with a number drops NaN), and the product with z makes that lane's
+// result NaN again. BLOCK: values read back from a checkpoint, whose blocks are NaN
+// throughout or not at all, go without the minimum (16384 x 12288 stored and read back
+// through the GELU: 204.2 us, 207.8 with it).
 template <int ACT>
 struct ActCoef;
 template <>
@@ -149,8 +151,9 @@ struct ActCoef<MF_ACT_SILU> {
   static constexpr float d1 = 1.f, d3 = 0.f;
 };
 
+// sigma(w(z)), and e.
 template <int ACT, bool BLOCK>
-__device__ __forceinline__ uint64_t act_sigma2(uint64_t z, uint64_t zz) {
+__device__ __forceinline__ uint64_t act_sigma2(uint64_t z, uint64_t zz, uint64_t& e) {
   using C = ActCoef<ACT>;
   const uint64_t v = ACT == MF_ACT_GELU
                          ? f2_mul(z, f2_fma(zz, f2_both(C::v3), f2_both(C::v1)))
@@ -161,8 +164,8 @@ __device__ __forceinline__ uint64_t act_sigma2(uint64_t z, uint64_t zz) {
     a = fminf(a, 62.f);
     b = fminf(b, 62.f);
   }
-  a = 1.f + ex2_approx(a);
-  b = 1.f + ex2_approx(b);
+  e = f2_pack(ex2_approx(a), ex2_approx(b));
+  f2_unpack(f2_add(e, f2_both(1.f)), a, b);
   const float r = rcp_approx(a * b);
   return f2_mul(f2_both(r), f2_pack(b, a));
 }
@@ -172,9 +175,10 @@ __device__ __forceinline__ uint64_t act_fwd2(uint64_t z) {
   if constexpr (ACT == MF_ACT_NONE) return z;
   else {
     float a, b;
+    uint64_t e;
     f2_unpack(z, a, b);
     z = f2_pack(max_nan(a, ActCoef<ACT>::low), max_nan(b, ActCoef<ACT>::low));
-    return f2_mul(z, act_sigma2<ACT, BLOCK>(z, f2_mul(z, z)));
+    return f2_mul(z, act_sigma2<ACT, BLOCK>(z, f2_mul(z, z), e));
   }
 }
 
@@ -182,14 +186,14 @@ template <int ACT>
 __device__ __forceinline__ uint64_t act_grad2(uint64_t z) {
   using C = ActCoef<ACT>;
   float a, b;
+  uint64_t e;
   f2_unpack(z, a, b);
   z = f2_pack(min_nan(max_nan(a, C::low), 30.f), min_nan(max_nan(b, C::low), 30.f));
   const uint64_t zz = f2_mul(z, z);
-  const uint64_t s = act_sigma2<ACT, false>(z, zz);
+  const uint64_t s = act_sigma2<ACT, false>(z, zz, e);
   uint64_t zd = z;  // z w'
   if constexpr (ACT == MF_ACT_GELU) zd = f2_mul(z, f2_fma(zz, f2_both(C::d3), f2_both(C::d1)));
-  // s + z w' (s - s^2)
-  return f2_fma(zd, f2_fma(f2_mul(s, f2_both(-1.f)), s, s), s);
+  return f2_fma(zd, f2_mul(f2_mul(e, s), s), s);
 }
 
 // The checkpoint kernels: CTAs of 256 threads, sixteen lanes to a block of 128

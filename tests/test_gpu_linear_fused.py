@@ -489,3 +489,47 @@ def test_a_nan_channel_stays_alone(pack, act, n0):
     check_bf16(dW[1, others], rdW[1, others], tol[1, others], "dW of the text")
     tol = (T + 8) * 2.0 ** -24 * adb + sdb
     assert (np.abs(db - rdb)[0] <= tol[0]).all() and (np.abs(db - rdb)[1, others] <= tol[1, others]).all()
+
+
+@pytest.mark.parametrize("mixed", [False, True], ids=["in_order", "mixed"])
+@pytest.mark.parametrize("z8", [False, True], ids=["bf16", "8bit"])
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_activation_gradient_to_fp32_at_every_magnitude(act, z8, mixed):
+    """db of one token with dout = 1 is act'(z) in fp32, from -100 to 100. In units u =
+    2^-24, with sigma = 1 / (1 + e), e = 2^v, act' = sigma + z w' e sigma^2: v is a
+    product of four roundings (4u), 2^v is good to 4u (its instruction) and 4u |v| ln 2,
+    1 + e to u beside e's, its reciprocal, shared by two values, to 4u. Beyond the ends
+    of the range where act' is held it is within 1e-15 of its limits."""
+    z = np.concatenate([np.linspace(-100, 100, 1024), np.linspace(-10, 10, 1536), np.linspace(6, 45, 384)])
+    if mixed:  # small and large ones side by side
+        z = np.random.default_rng(11).permutation(z)
+    z = bf16(z.astype(np.float32))[None, :]
+    N, u = z.shape[1], 2.0 ** -24
+    tm = torch.zeros(1, dtype=torch.uint8, device="cuda")
+    ones = torch.ones((1, N), dtype=torch.bfloat16, device="cuda")
+    zt = zq = zs = None
+    zv = _f64(z)
+    if z8:
+        zq, zs, zv = _code(z)
+    else:
+        zt = dev(z)
+    db = torch.empty((2, N), device="cuda")
+    n = mf.mf_linear_fused_bwd_workspace_size(1, 8, N)
+    mf.mf_linear_fused_bwd(ones, None, None, None, None, zt, zq, zs, tm, ((1, 1, 1, 0),), 8, N, ACTS[act],
+                           None, None, db, torch.empty(n, dtype=torch.uint8, device="cuda"), n)
+    assert mf.mf_get_error() == mf.MF_OK and (db[1] == 0).all()
+    c1, c3 = (2 * np.sqrt(2 / np.pi), 2 * np.sqrt(2 / np.pi) * 0.044715) if act == "gelu" else (1.0, 0.0)
+    w = zv * (c1 + c3 * zv * zv)
+    s = 1 / (1 + np.exp(-np.clip(w, -700, 700)))
+    e = 4 * u * np.abs(w) + 4 * u
+    es = (1 - s) * e + 5 * u
+    ref = oracle.mlp_act_grad(zv, act)
+    zw = np.abs(zv * (c1 + 3 * c3 * zv * zv))
+    turn = zw * s * (1 - s)
+    tol = 1.01 * (s * es + turn * (e + 2 * es + 6 * u) + u * np.abs(ref)) + 1e-15
+    # the oracle's own: tanh is rounded by 2^-54 just below 1, 1 - tanh^2 so by 2^-53
+    # beside its own rounding, and it enters times z w' / 2
+    tol = tol + 2.0 ** -53 * zw
+    err = np.abs(host(db)[0] - ref[0])
+    i = int(np.argmax(err - tol[0]))
+    assert err[i] <= tol[0, i], f"z {zv[0, i]}: off by {err[i]:.3g}, tolerance {tol[0, i]:.3g}"
