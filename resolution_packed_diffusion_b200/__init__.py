@@ -136,7 +136,7 @@ def _ptr(t) -> Optional[int]:
     """Device pointer of a contiguous CUDA tensor (None -> NULL)."""
     if t is None:
         return None
-    if type(t) is int:
+    if isinstance(t, int):
         return t
     if not t.is_cuda:
         raise ValueError("libmf entry points take device tensors")

@@ -119,3 +119,17 @@ def test_binding_takes_a_descriptor_array():
     assert mf._descs(arr) == (arr, 2)
     got, n = mf._descs([(1, 2, 2, 3), (0, 0, 0, 5)])
     assert n == 2 and [(d.frames, d.n_text) for d in got] == [(1, 3), (0, 5)]
+
+
+def test_binding_takes_subclasses_of_int_as_addresses():
+    """A pointer may come as any int, an enum's or a library's own type too."""
+    class Address(int):
+        pass
+
+    assert mf._ptr(Address(A[0])) == A[0] and mf._ptr(A[0]) == A[0] and mf._ptr(None) is None
+    mf.mf_layer_norm(Address(A[0]), Address(A[1]), Address(A[2]), Address(A[3]), 0, 256, 1e-6,
+                     Address(A[4]), Address(A[5]), stream=Address(0))
+    with pytest.raises(mf.MFError) as e:  # reaches the library, which finds x and y the same
+        mf.mf_layer_norm(Address(A[0]), Address(A[1]), Address(A[2]), Address(A[3]), 4, 256, 1e-6,
+                         Address(A[0]), stream=0)
+    assert e.value.status == INV
