@@ -447,9 +447,9 @@ mf_status mf_linear_fused(const mf_bf16* x, const mf_bf16* W, const float* bias,
  * both products (db sums it unrounded), an 8-bit x is rounded to bf16 as an
  * operand; fp32 accumulation in a fixed order, no atomics. Rows of the other
  * modality take no part in dW[m] whatever they hold. No output overlaps anything
- * else. ws_bytes >= mf_linear_fused_bwd_workspace_size(T, K, N). Shapes, tok_mod
- * and desc as for the forward (a tok_mod above 1 is recorded as MF_ERR_INVALID
- * where db or act' is computed). */
+ * else. ws_bytes >= mf_linear_fused_bwd_workspace_size(T, K, N), which does not fall
+ * as T grows. Shapes, tok_mod and desc as for the forward (a tok_mod above 1 is
+ * recorded as MF_ERR_INVALID where db or act' is computed). */
 mf_status mf_linear_fused_bwd(const mf_bf16* dout, const mf_bf16* x, const int8_t* x8,
                               const float* x_scale, const mf_bf16* W, const mf_bf16* z,
                               const int8_t* z8, const float* z_scale, const uint8_t* tok_mod,

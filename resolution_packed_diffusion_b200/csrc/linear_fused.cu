@@ -817,6 +817,13 @@ constexpr int kDzUnroll = 4;
 
 // Short packs get short chunks, so that there are CTAs for every SM.
 int dz_rows(int32_t T) { return T <= 2048 ? 32 : T <= 8192 ? 64 : 128; }
+int dz_chunks(int32_t T) { return (T + dz_rows(T) - 1) / dz_rows(T); }
+// The most chunks of any pack of up to T tokens: what the workspace is sized by, so that
+// one taken for a long pack serves shorter ones.
+int dz_chunks_most(int32_t T) {
+  const int least = T <= 2048 ? 0 : dz_chunks(T <= 8192 ? 2048 : 8192);
+  return dz_chunks(T) > least ? dz_chunks(T) : least;
+}
 
 struct Decode {
   Act8 x8;
@@ -1164,7 +1171,7 @@ cudaError_t launch_linear_fused(const mf_bf16* x, const mf_bf16* W, const TokenR
 // Workspace, in this order: dz [T][N] bf16; db's partials; an 8-bit x in bf16; dW's
 // parts.
 size_t linear_fused_bwd_ws(int32_t T, int32_t K, int32_t N) {
-  const size_t chunks = static_cast<size_t>((T + dz_rows(T) - 1) / dz_rows(T));
+  const size_t chunks = dz_chunks_most(T);
   const size_t parts = dw_tiles(K, N, kTile) * 2 <= kPairs ? static_cast<size_t>(2) * kPairs : 0;
   return round256(static_cast<size_t>(T) * N * 2) + round256(chunks * 2 * N * sizeof(float)) +
          round256(static_cast<size_t>(T) * K * 2) + parts * kTile * kTile * sizeof(float);
@@ -1175,7 +1182,7 @@ cudaError_t launch_linear_fused_bwd(const LinearBwd& b, const TokenRuns& runs, i
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
   mf_bf16* dz_ws = reinterpret_cast<mf_bf16*>(w);
   w += round256(static_cast<size_t>(T) * N * 2);
-  const int rows = dz_rows(T), chunks = (T + rows - 1) / rows;
+  const int rows = dz_rows(T), chunks = dz_chunks(T);
   float* part = reinterpret_cast<float*>(w);
   w += round256(static_cast<size_t>(chunks) * 2 * N * sizeof(float));
   mf_bf16* x_ws = reinterpret_cast<mf_bf16*>(w);

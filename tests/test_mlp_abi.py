@@ -133,3 +133,16 @@ def test_binding_takes_subclasses_of_int_as_addresses():
         mf.mf_layer_norm(Address(A[0]), Address(A[1]), Address(A[2]), Address(A[3]), 4, 256, 1e-6,
                          Address(A[0]), stream=0)
     assert e.value.status == INV
+
+
+@pytest.mark.parametrize("a,b", [(8, 8), (128, 512), (1000, 2056), (12288, 3080)])
+def test_a_workspace_for_a_long_pack_serves_a_shorter_one(a, b):
+    """The sizes never fall as T grows: a buffer taken for the largest pack is enough for
+    every other."""
+    lengths = sorted({max(1, c + d) for c in (1, 64, 128, 544, 2048, 4096, 8192, 16384, 131072)
+                      for d in (-129, -65, -33, -1, 0, 1, 33, 65, 129) if c + d <= 131072})
+    sizes = [mf.mf_linear_fused_bwd_workspace_size(t, a, b) for t in lengths]
+    assert sizes[0] > 0 and sizes == sorted(sizes)
+    for width in (8, 264, 1000, 3000, 8192):
+        sizes = [mf.mf_layer_norm_bwd_workspace_size(t, width) for t in lengths]
+        assert sizes[0] > 0 and sizes == sorted(sizes)
