@@ -1084,6 +1084,14 @@ int dw_splits(int tiles, int steps) {
   return p > 1 && steps - (steps + p - 1) / p >= kDwJoinSteps ? p : 1;
 }
 
+// The most steps that one modality of a pack of T tokens can have: a run ends in at most
+// one step that it does not fill, and a token of the other modality at least lies between
+// two runs.
+int dw_steps_most(int32_t T) {
+  const int32_t runs = (T + 1) / 2;
+  return T / kStepK + (runs < MF_MAX_SAMPLES ? runs : MF_MAX_SAMPLES);
+}
+
 // Column width of dW's tiles: 256 if a modality's steps are split, and otherwise
 // narrower only while its tiles and the launch's others (`sets` modalities, `dx`) fit
 // one round: a step takes as long at any width, so narrow tiles in several rounds lose
@@ -1172,7 +1180,8 @@ cudaError_t launch_linear_fused(const mf_bf16* x, const mf_bf16* W, const TokenR
 // parts.
 size_t linear_fused_bwd_ws(int32_t T, int32_t K, int32_t N) {
   const size_t chunks = dz_chunks_most(T);
-  const size_t parts = dw_tiles(K, N, kTile) * 2 <= kPairs ? static_cast<size_t>(2) * kPairs : 0;
+  const int tiles = dw_tiles(K, N, kTile), splits = dw_splits(tiles, dw_steps_most(T));
+  const size_t parts = splits > 1 ? static_cast<size_t>(2) * tiles * splits : 0;
   return round256(static_cast<size_t>(T) * N * 2) + round256(chunks * 2 * N * sizeof(float)) +
          round256(static_cast<size_t>(T) * K * 2) + parts * kTile * kTile * sizeof(float);
 }

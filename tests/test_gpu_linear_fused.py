@@ -533,3 +533,27 @@ def test_activation_gradient_to_fp32_at_every_magnitude(act, z8, mixed):
     err = np.abs(host(db)[0] - ref[0])
     i = int(np.argmax(err - tol[0]))
     assert err[i] <= tol[0, i], f"z {zv[0, i]}: off by {err[i]:.3g}, tolerance {tol[0, i]:.3g}"
+
+
+@pytest.mark.parametrize("descs", [tuple((1, 1, 1, 1) for _ in range(n)) for n in (23, 24, 25, 48, 49, 130, 512)]
+                         + [tuple((1, 1, 65, 66) for _ in range(256)), ((1, 12, 64, 769),), ((0, 0, 0, 1537),)])
+def test_backward_stays_in_its_workspace(descs):
+    """Packs with the most steps for their tokens, around the first that has dW in parts:
+    exactly the bytes asked for, with a pattern behind them."""
+    K, N = 8, 264
+    d = _data(descs, K, N, 91)
+    T, n = d["T"], mf.mf_linear_fused_bwd_workspace_size(d["T"], K, N)
+    ws = torch.full((n + (48 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+    dx = torch.empty((T, K), dtype=torch.bfloat16, device="cuda")
+    dW = torch.empty((2, N, K), dtype=torch.bfloat16, device="cuda")
+    db = torch.empty((2, N), device="cuda")
+    xq, xs, xv = _code(d["x"])
+    mf.mf_linear_fused_bwd(dev(d["dout"]), None, xq, xs, dev(d["W"]), None, None, None,
+                           torch.from_numpy(d["mod"]).cuda(), descs, K, N, 0, dx, dW, db, ws, n)
+    assert mf.mf_get_error() == mf.MF_OK
+    assert (ws[n:] == 0x5A).all(), "bytes behind the workspace were written"
+    rdx, rdW, rdb, dz = oracle.linear_fused_bwd(d["dout"], xv, d["W"], None, d["mod"], "none")
+    adx, adW, adb, _ = oracle.linear_fused_bwd(np.abs(dz), np.abs(xv), np.abs(d["W"]), None, d["mod"], "none")
+    check_bf16(host(dx), rdx, adx * (N + 2) * 2.0 ** -23, "dx")
+    check_bf16(host(dW), rdW, adW * (2.0 ** -8 + (T + 64) * 2.0 ** -23), "dW")
+    assert (np.abs(host(db) - rdb) <= (T + 8) * 2.0 ** -24 * adb).all()

@@ -146,3 +146,14 @@ def test_a_workspace_for_a_long_pack_serves_a_shorter_one(a, b):
     for width in (8, 264, 1000, 3000, 8192):
         sizes = [mf.mf_layer_norm_bwd_workspace_size(t, width) for t in lengths]
         assert sizes[0] > 0 and sizes == sorted(sizes)
+
+
+def test_the_linear_backward_asks_for_the_memory_that_it_can_use():
+    """Few tokens cannot have dW's sum cut into parts, whose places are 256 KB each; a long
+    pack and one of many short runs can, of a narrow layer."""
+    size = mf.mf_linear_fused_bwd_workspace_size
+    for t in (1, 16, 40):
+        for k, n in ((8, 8), (128, 512), (512, 128)):
+            assert size(t, k, n) < 4 * t * (k + n) + 8 * n * t + 2048
+    for t in (1024, 16384):  # up to 512 runs, each with a step of its own
+        assert size(t, 128, 512) >= 2 * 2 * 37 * 256 * 256 * 4
