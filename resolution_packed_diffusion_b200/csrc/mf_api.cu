@@ -28,7 +28,6 @@ constexpr int kMaxDevices = 64;
 constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;
 
 struct DeviceState {
-  bool ready = false;
   int* err = nullptr;
   uint64_t wait_limit_ns = kDefaultWaitLimitNs;
   cudaEvent_t attn_start = nullptr;  // instrumentation (mf_set_attn_timing_events)
@@ -159,15 +158,19 @@ cudaError_t get_ctl(KernelCtl* ctl) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  std::lock_guard<std::mutex> lock(g_mutex);
-  DeviceState& d = g_state[dev];
-  if (!d.ready) {
-    void* p = nullptr;
+  // A host thread has no CUDA context before its first runtime call that needs one, and
+  // tensor maps are encoded by the driver, which then refuses: so each thread asks for the
+  // symbol once per device.
+  static thread_local uint64_t seen = 0;
+  void* p = nullptr;
+  if (!((seen >> dev) & 1)) {
     e = cudaGetSymbolAddress(&p, g_mf_error);
     if (e != cudaSuccess) return e;
-    d.err = static_cast<int*>(p);
-    d.ready = true;
+    seen |= uint64_t{1} << dev;
   }
+  std::lock_guard<std::mutex> lock(g_mutex);
+  DeviceState& d = g_state[dev];
+  if (p != nullptr) d.err = static_cast<int*>(p);
   ctl->err = d.err;
   ctl->wait_limit_ns = d.wait_limit_ns;
   return cudaSuccess;
