@@ -51,19 +51,26 @@ __device__ __forceinline__ uint4 bf16x8_pack(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
-// Eight codes as values. Byte b ^ 0x80 in the low mantissa bits of 2^23 is
+// Eight codes as numbers. Byte b ^ 0x80 in the low mantissa bits of 2^23 is
 // 2^23 + b + 128, exactly: one byte permute a value and one subtraction a pair, off
 // the quarter-rate integer conversion path.
-__device__ __forceinline__ void act8_load(const uint2& q, float s, uint64_t (&f)[4]) {
+__device__ __forceinline__ void act8_codes(const uint2& q, uint64_t (&f)[4]) {
   const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
-  const uint64_t bias = f2_both(-8388736.f), s2 = f2_both(s);
+  const uint64_t bias = f2_both(-8388736.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t u = w[i >> 1];
     const uint32_t lo = __byte_perm(u, 0x4B000000u, (i & 1) ? 0x7442 : 0x7440);
     const uint32_t hi = __byte_perm(u, 0x4B000000u, (i & 1) ? 0x7443 : 0x7441);
-    f[i] = f2_mul(f2_add(f2_pack(__uint_as_float(lo), __uint_as_float(hi)), bias), s2);
+    f[i] = f2_add(f2_pack(__uint_as_float(lo), __uint_as_float(hi)), bias);
   }
+}
+
+// Eight codes as the values they stand for.
+__device__ __forceinline__ void act8_load(const uint2& q, float s, uint64_t (&f)[4]) {
+  act8_codes(q, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = f2_mul(f[i], f2_both(s));
 }
 
 // Scale and reciprocal step of a block whose largest |x| is `amax` (its bit

@@ -472,12 +472,12 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
   uint32_t parity = 0;
   fetch(row);
   for (int s = 0; s < steps; ++s, row += step, out += out_step) {
-    float2 st[R];  // (-mean * rstd, rstd)
+    float2 st[R];  // (-mean, rstd)
     float sc[R][CH];
     int mod[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      st[i] = make_float2(-nst[i].x * nst[i].y, nst[i].y);
+      st[i] = make_float2(-nst[i].x, nst[i].y);
 #pragma unroll
       for (int j = 0; j < CH; ++j) sc[i][j] = nsc[i][j];
       mod[i] = nmod[i];
@@ -496,14 +496,22 @@ __global__ void __launch_bounds__(THREADS, PER_SM) layer_norm_bwd_kernel(
     (void)mbar_wait(&full[at], parity, a.ctl, abort_flag);
     auto operands = [&](int i, int j, uint64_t (&h)[4], uint64_t (&d)[4]) {
       const uint32_t o = i * a.hid + j * chunk;
-      if constexpr (X8)
-        act8_load(*reinterpret_cast<const uint2*>(sx + o), sc[i][j], h);
-      else
-        bf16x8_f2(*reinterpret_cast<const uint4*>(sx + 2 * o), h);
-      bf16x8_f2(*reinterpret_cast<const uint4*>(sd + 2 * o), d);
+      // (x - mean) rstd, the difference first: x rstd - mean rstd would leave the rounding of
+      // a product where x is near the mean (one instruction a pair less: 65.4 against
+      // 66.7 us at 16384 x 3072 from bf16, no difference with a residual or from 8 bits)
       const uint64_t r2 = f2_both(st[i].y), m2 = f2_both(st[i].x);
+      if constexpr (X8) {
+        act8_codes(*reinterpret_cast<const uint2*>(sx + o), h);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = f2_fma(h[e], r2, m2);
+        for (int e = 0; e < 4; ++e) h[e] = f2_fma(h[e], f2_both(sc[i][j]), m2);
+      } else {
+        bf16x8_f2(*reinterpret_cast<const uint4*>(sx + 2 * o), h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = f2_add(h[e], m2);
+      }
+      bf16x8_f2(*reinterpret_cast<const uint4*>(sd + 2 * o), d);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = f2_mul(h[e], r2);
     };
     float sums[2 * R];
     auto accumulate = [&](int i) {

@@ -334,3 +334,31 @@ def test_a_backward_whose_waits_run_out_leaves_nothing_behind(hid, ckpt):
         mf.mf_set_wait_limit_ns(2_000_000_000)
     for got, ref in zip(_bwd(dy, x, gamma, st, mod, resid, ckpt=ckpt), want):
         assert np.array_equal(got, ref)
+
+
+@pytest.mark.parametrize("ckpt", [False, True], ids=["bf16", "act8"])
+@pytest.mark.parametrize("hid", [136, 1000, 2048, 3000])
+def test_backward_of_constant_rows(hid, ckpt):
+    """Rows that hold one value: xhat is what x and the mean leave, 0 from bf16, and not the
+    rounding of mean * rstd (up to 0.016 at 300 with an rstd near 1000)."""
+    mod = modalities(MIXED)
+    T = len(mod)
+    rng = np.random.default_rng(hid)
+    x = bf16(np.repeat(rng.choice([300.0, -299.0, 87.5, 0.0], (T, 1)), hid, 1))
+    xv = oracle.act8_values(*oracle.act8_quantize(x)) if ckpt else _f64(x)
+    dy = bf16(rng.standard_normal((T, hid)))
+    gamma = np.float32(1 + 0.1 * rng.standard_normal((2, hid)))
+    st = np.float32(np.stack([xv[:, 0], np.full(T, 999.4321)], 1))
+    dx, dg, db = _bwd(dy, x, gamma, st, mod, ckpt=ckpt)
+    rdx, rdg, rdb = oracle.layer_norm_affine_bwd(dy, xv, gamma, st, mod)
+    s64 = _f64(st)
+    xhat, g = np.abs((xv - s64[:, :1]) * s64[:, 1:]), np.abs(dy * _f64(gamma)[mod])
+    # x - mean is exact here, xhat one rounding of it; the row sums are off by at most 64
+    # units of their sums of magnitudes, then a few roundings
+    m1, m2 = g.mean(1, keepdims=True), (g * xhat).mean(1, keepdims=True)
+    check_bf16(dx, rdx, 2.0 ** -24 * s64[:, 1:] * (8 * g + 72 * m1 + 72 * xhat * m2), "dx")
+    for got, ref, terms in ((dg, rdg, np.abs(dy) * xhat), (db, rdb, np.abs(dy))):
+        mags = np.stack([terms[mod == m].sum(0) for m in (0, 1)])
+        assert (np.abs(got - ref) <= (T + 8) * 2.0 ** -24 * mags).all()
+    if not ckpt:
+        assert (dg == 0).all()
