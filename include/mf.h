@@ -513,7 +513,8 @@ mf_status mf_get_error(cudaStream_t stream);
 
 /* Limit, in nanoseconds, of every device-side wait of later launches on the
  * current device (default 2e9). A wait that runs out records MF_ERR_TIMEOUT,
- * and the kernel winds down and returns. */
+ * and the kernel winds down and returns; in the layer norm's backward and the
+ * fused linear layer it waits 50 ms at least for copies of its own under way. */
 mf_status mf_set_wait_limit_ns(uint64_t ns);
 
 /* Attention kernel of later calls of mf_varlen_attn_fwd, mf_block_fwd and

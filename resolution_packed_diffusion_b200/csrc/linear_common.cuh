@@ -98,10 +98,10 @@ __device__ __forceinline__ uint64_t keep_in_l2() {
 }
 
 // Waits for copies or MMAs in flight before their shared memory is used otherwise or the
-// CTA leaves. At least a second, however short the limit of the other waits: a copy that
+// CTA leaves. At least 50 ms, however short the limit of the other waits: a copy that
 // lands after its CTA has left writes to memory that is someone else's.
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-  constexpr uint64_t kLeastNs = 1000000000ull;
+  constexpr uint64_t kLeastNs = 50000000ull;
   const uint64_t limit = limit_ns > kLeastNs ? limit_ns : kLeastNs;
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity))
